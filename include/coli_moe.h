@@ -355,6 +355,176 @@ int64_t coli_alloc_bytes(void);
  * a device or if the launch fails.  bytes == 0 launches nothing. */
 coli_status coli_probe_read(const void *buf, size_t bytes, uint32_t *sink, void *stream);
 
+/* ---------------------------------------------------------------------------
+ * Serving operators beside the expert layer: the attention of the same
+ * decoder layer over a cache of latent vectors (the pages' compressed
+ * attention state: 576 values per token in place of 32,768, README "Come
+ * funziona"), and the verification of the drafted tokens that the calls of a
+ * few tokens exist for.
+ *
+ * A cached token is one row of 576 16-bit values: 512 latent values, which are
+ * both key and value of every head, and 64 rotary key values.  Rows live in
+ * pages of page_size rows; row i of page p is at element p * page_stride +
+ * i * 576 of the cache.  A sequence's pages are listed in its row of the block
+ * table: position s is row s % page_size of page table[s / page_size].
+ *
+ *   coli_latent_append  writes the rows of new tokens (norm, rotary part) and
+ *                       rotates the same tokens' queries.
+ *   coli_latent_plan    divides a step's attention over the CUs, once per step
+ *                       for the calls of all its layers.
+ *   coli_latent_decode  absorbed attention of single, chained or tree-drafted
+ *                       tokens over the cache.
+ *   coli_latent_prompt  expanded attention of whole prompts.
+ *   coli_draft_verify   accepts drafted tokens and samples the next one.
+ *   coli_latent_keep    moves the accepted nodes' rows together.
+ *
+ * The tokens of a call are those of its sequences one after the other: the
+ * tokens of sequence b are q_start[b] .. q_start[b + 1] - 1 (int32
+ * [n_seq + 1], ascending, within 0..n_tok; tokens that no sequence covers are
+ * left alone).  Every array argument is device memory of the caller's; rows,
+ * strides in elements.  A value that only the device can see to be outside
+ * its bounds is not an error return: it sets a bit in the handle's device
+ * error flags, nothing outside the buffers is read or written, and the
+ * outputs of the sequences concerned are unspecified.  Calls on one handle
+ * share its plan and scratch and must not overlap in time. */
+typedef enum { COLI_HALF_BF16 = 0, COLI_HALF_F16 = 1 } coli_half;
+typedef enum { COLI_PROB_F32 = 0, COLI_PROB_BF16 = 1, COLI_PROB_F16 = 2 } coli_prob;
+
+typedef struct {
+    int32_t n_heads;     /* query heads, 1..1024 */
+    int32_t latent;      /* 512 */
+    int32_t rope;        /* 64 */
+    int32_t nope;        /* expanded head: non-rotary key width, 192 or 128 */
+    int32_t v_dim;       /* expanded head: value width, 256 (nope 192) or 128 (nope 128) */
+    int32_t page_size;   /* rows per cache page: a power of two up to 65536 */
+    int32_t max_tokens;  /* largest n_tok (or n_q) any call will pass */
+    int32_t max_seqs;    /* largest n_seq any call will pass */
+    int32_t half;        /* coli_half: type of queries, cache, keys, values and outputs */
+} coli_serve_dims;
+
+typedef struct coli_serve coli_serve;   /* opaque, library-owned */
+
+/* Create a handle on HIP device `device`: the plan, the partial results of
+ * split attention (four per CU of 128 KB: 134 MB on 256 CUs) and the scratch
+ * of verification.  COLI_E_INVALID for bad dims, COLI_E_UNSUPPORTED for sizes
+ * the kernels do not handle (other latent, rope, nope and v_dim widths;
+ * max_tokens * n_heads over 2^30; max_seqs over 2^20), COLI_E_NOMEM,
+ * COLI_E_DEVICE.  *out is set only on success. */
+coli_status coli_serve_create(const coli_serve_dims *dims, int device, coli_serve **out);
+/* Free everything the handle owns.  NULL is accepted.  Synchronises the device. */
+coli_status coli_serve_destroy(coli_serve *serve);
+/* Message of the last failed call on the handle (NULL: of the last failed
+ * coli_serve_create of this thread). */
+const char *coli_serve_last_error(const coli_serve *serve);
+/* Read and clear the device error flags (synchronises the device):
+ *   bit 0 (1) = q_start, k_start or kv_len outside the call's tokens or keys,
+ *               or a sequence of more than 1024 drafted nodes in coli_draft_verify;
+ *   bit 1 (2) = a page number, slot or position outside the cache, block
+ *               table or rotary table;
+ *   bit 2 (4) = a drafted token, parent or path entry out of range;
+ *   bit 3 (8) = a row of probabilities with no positive one. */
+coli_status coli_serve_device_errors(coli_serve *serve, int32_t *flags);
+
+/* Append.  For token t with c = row t of `c` ([n_tok x 576], row stride
+ * c_stride):
+ *   latent = c[0..511] / sqrt(mean(c[0..511]^2) + eps) * norm_weight,
+ *   rotary = c[512..575] with each pair (a, b) turned to
+ *            (a cos - b sin, a sin + b cos): pairs (2i, 2i + 1) if
+ *            interleaved, else (i, i + 32), angles from row positions[t] of the fp32
+ *            tables cos_table and sin_table ([n_positions x 32]),
+ * computed in fp32 and rounded once into cache row slots[t] (int64, page *
+ * page_size + row; negative: the token is not cached).  Slots of one call are
+ * distinct.  With q_pe ([n_tok x n_heads x 64], strides q_tok_stride and
+ * q_head_stride) non-NULL the tokens' rotary query parts are turned by the
+ * same angles into q_out ([n_tok x n_heads x 64], contiguous, not
+ * overlapping q_pe unless it is the same contiguous array).
+ * Pointers 16-byte aligned, strides multiples of 8 elements. */
+coli_status coli_latent_append(coli_serve *serve, const void *c, int64_t c_stride, const void *norm_weight, float eps,
+                               const float *cos_table, const float *sin_table, int32_t n_positions, int32_t interleaved,
+                               const int32_t *positions, const int64_t *slots, int32_t n_tok, void *cache, int64_t page_stride,
+                               int32_t n_pages, const void *q_pe, int64_t q_tok_stride, int64_t q_head_stride, void *q_out,
+                               void *stream);
+
+/* Plan the absorbed attention of a step: sequence b has its q_start[b + 1] -
+ * q_start[b] tokens of this step as the last of kv_len[b] cached positions
+ * (kv_len may be smaller, even 0: the leading tokens then see nothing).  The plan
+ * is made on the device and kept in the handle: every later coli_latent_decode
+ * uses it, until the next one.  q_start and kv_len are read by this call alone. */
+coli_status coli_latent_plan(coli_serve *serve, const int32_t *q_start, const int32_t *kv_len, int32_t n_seq, int32_t n_tok,
+                             void *stream);
+
+/* Absorbed attention of the planned step.  Token i of a sequence (of n) and
+ * head h: s_j = scale (q_lat . latent_j + q_pe . rotary_j) over the cached
+ * positions j it sees, out = sum_j softmax(s)_j latent_j ([n_tok x n_heads x
+ * 512], contiguous), lse (fp32 [n_tok x n_heads], may be NULL) = log sum_j
+ * exp(s_j).  It sees every position before the step's tokens, and of those
+ *   tree_mask NULL: the tokens up to itself (a chain);
+ *   else: the tokens m whose bit m % 64 of word m / 64 of its row of
+ *         tree_mask ([n_tok x mask_words] 64-bit words) is set: itself and
+ *         its ancestors; tokens past the words are not seen.
+ * A token that sees nothing gets zeros and lse = -inf.  Cached rows that a
+ * token does not see have no part in its result, whatever they hold.
+ * COLI_E_STATE before the first plan.  Pointers 16-byte aligned, strides multiples
+ * of 8 elements. */
+coli_status coli_latent_decode(coli_serve *serve, const void *q_lat, int64_t ql_tok_stride, int64_t ql_head_stride,
+                               const void *q_pe, int64_t qp_tok_stride, int64_t qp_head_stride, const void *cache,
+                               int64_t page_stride, int32_t n_pages, const int32_t *block_table, int64_t table_stride,
+                               int32_t table_cols, const uint64_t *tree_mask, int32_t mask_words, float scale, int32_t n_tok,
+                               void *out, float *lse, void *stream);
+
+/* Expanded attention of whole prompts.  q [n_q x n_heads x (nope + 64)] (rotary
+ * part last, already turned), kv [n_k x n_heads x (nope + v_dim)] (each head's
+ * non-rotary key, then its value, as the up-projection leaves them), k_pe
+ * [n_k x 64] the rotary keys shared by the heads.  Sequence b has queries
+ * q_start[b] .. and keys k_start[b] .. (int32 [n_seq + 1] each); with
+ * causal = 1 its queries are the last of its keys' positions (query i of n
+ * sees key j of m if j <= i + m - n), with 0 every query sees every key.
+ * out [n_q x n_heads x v_dim] contiguous, lse as in coli_latent_decode; a
+ * query that sees nothing gets zeros and -inf.  Keys and values that a query does not
+ * see have no part in its result, whatever they hold; an output whose seen
+ * values are not all finite may be NaN where they would sum to an infinity. */
+coli_status coli_latent_prompt(coli_serve *serve, const void *q, int64_t q_tok_stride, int64_t q_head_stride, const void *kv,
+                               int64_t kv_tok_stride, int64_t kv_head_stride, const void *k_pe, int64_t pe_tok_stride,
+                               const int32_t *q_start, const int32_t *k_start, int32_t n_seq, int32_t n_q, int32_t n_k,
+                               int32_t causal, float scale, void *out, float *lse, void *stream);
+
+/* Verify drafted tokens.  Node 0 of a sequence is its last accepted token, node j
+ * (j >= 1) a drafted one, tokens[] their ids, parents[j] (index within the
+ * sequence, < j) the node it continues; parents NULL: node j continues node
+ * j - 1.  Row t of probs ([n_tok x vocab] of `kind`, row stride probs_stride)
+ * holds the target's probabilities after node t, row t of draft (or NULL)
+ * those that the children of node t were drawn from.  From node 0 on, the
+ * children x of a node are tried in index order with u[] (fp32 in [0, 1)) of
+ * the child: after k refusals
+ *   with draft row q:  taken if u q(x) Z_k < (p - a_k q)+(x), where a_0 = 0,
+ *                      Z_0 = 1, a_{k+1} = a_k + Z_k, Z_k = sum (p - a_k q)+;
+ *   without:           taken if u Z_k < p(x) (0 if x was refused before),
+ *                      Z_k = 1 - the refused tokens' probability.
+ * Where no child is taken the next token is the lowest index with the largest
+ * r race, r = p before any refusal, else (p - a_k q)+ or p without the refused
+ * tokens (p itself should that be zero everywhere), race = row b of the fp32
+ * [n_seq x vocab] array, 1 / Exp(1) variates: a draw from r.
+ * Outputs, int32: path [n_seq x path_cols] the nodes taken, node 0 first,
+ * then -1; count [n_seq] their number; next_tokens [n_seq x path_cols] the
+ * tokens of path[1..] and the sampled one, then -1.  A path longer than path_cols
+ * ends there.  A sequence without nodes has count 0.  Probabilities that are
+ * negative or NaN count as zero. */
+coli_status coli_draft_verify(coli_serve *serve, const void *probs, int64_t probs_stride, const void *draft, int64_t draft_stride,
+                              int32_t kind, int32_t vocab, const int32_t *tokens, const int32_t *parents, const int32_t *q_start,
+                              int32_t n_seq, int32_t n_tok, const float *u, const float *race, int64_t race_stride, int32_t *path,
+                              int32_t path_cols, int32_t *count, int32_t *next_tokens, void *stream);
+
+/* Keep the accepted nodes' rows: in each of n_layers caches (layer_stride
+ * elements apart, all with the same pages) the row of node path[b][i] of
+ * sequence b moves to node position i (position kv_len[b] - n + i of its n
+ * tokens), for i up to the first negative entry or path_cols.  Entries ascend, as
+ * coli_draft_verify writes them.  The sequence's next length is kv_len[b] - n
+ * + count[b]. */
+coli_status coli_latent_keep(coli_serve *serve, void *cache, int64_t page_stride, int32_t n_pages, int32_t n_layers,
+                             int64_t layer_stride, const int32_t *block_table, int64_t table_stride, int32_t table_cols,
+                             const int32_t *q_start, const int32_t *kv_len, int32_t n_seq, int32_t n_tok, const int32_t *path,
+                             int64_t path_stride, int32_t path_cols, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -22,7 +22,7 @@ PATH_AUTO, PATH_GEMV, PATH_GROUPED = 0, 1, 2
 SHARED = -1
 
 # Every function the header declares, with (restype, argtypes).
-_p, _i32, _sz, _i64 = C.c_void_p, C.c_int32, C.c_size_t, C.c_int64
+_p, _i32, _sz, _i64, _f = C.c_void_p, C.c_int32, C.c_size_t, C.c_int64, C.c_float
 SIGNATURES = {
     "coli_abi_version": (_i32, []),
     "coli_status_str": (C.c_char_p, [C.c_int]),
@@ -50,6 +50,20 @@ SIGNATURES = {
     "coli_set_alloc_limit": (C.c_int, [_i64]),
     "coli_alloc_bytes": (_i64, []),
     "coli_probe_read": (C.c_int, [_p, _sz, _p, _p]),
+    "coli_serve_create": (C.c_int, [_p, C.c_int, _p]),
+    "coli_serve_destroy": (C.c_int, [_p]),
+    "coli_serve_last_error": (C.c_char_p, [_p]),
+    "coli_serve_device_errors": (C.c_int, [_p, _p]),
+    "coli_latent_append": (C.c_int, [_p, _p, _i64, _p, _f, _p, _p, _i32, _i32, _p, _p, _i32, _p, _i64, _i32, _p, _i64, _i64,
+                                     _p, _p]),
+    "coli_latent_plan": (C.c_int, [_p, _p, _p, _i32, _i32, _p]),
+    "coli_latent_decode": (C.c_int, [_p, _p, _i64, _i64, _p, _i64, _i64, _p, _i64, _i32, _p, _i64, _i32, _p, _i32, _f, _i32,
+                                     _p, _p, _p]),
+    "coli_latent_prompt": (C.c_int, [_p, _p, _i64, _i64, _p, _i64, _i64, _p, _i64, _p, _p, _i32, _i32, _i32, _i32, _f, _p, _p,
+                                     _p]),
+    "coli_draft_verify": (C.c_int, [_p, _p, _i64, _p, _i64, _i32, _i32, _p, _p, _p, _i32, _i32, _p, _p, _i64, _p, _i32, _p, _p,
+                                    _p]),
+    "coli_latent_keep": (C.c_int, [_p, _p, _i64, _i32, _i32, _i64, _p, _i64, _i32, _p, _p, _i32, _i32, _p, _i64, _i32, _p]),
 }
 KERNEL_KINDS = ["router", "topk", "union", "plan", "gateup", "down", "combine"]
 

@@ -18,6 +18,7 @@
 
 #include "coli_moe.h"
 #include "internal.h"
+#include "serve.h"
 
 namespace coli {
 // probe.hip: the streaming-read reference kernel behind coli_probe_read.
@@ -254,6 +255,13 @@ void host_free(const void *p) {
 }
 
 }  // namespace
+}  // namespace coli
+
+// The same book for the serve handles (serve.hip).
+namespace coli {
+hipError_t book_alloc(void **p, size_t n) { return dev_alloc(p, n); }
+bool book_fits(size_t n) { return mem_fits(n); }
+void book_free(void *p) { dev_free(p); }
 }  // namespace coli
 
 // Scratch of coli_moe_layer_static, the entry point that allocates
