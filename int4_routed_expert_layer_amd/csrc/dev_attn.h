@@ -29,6 +29,16 @@ __device__ __forceinline__ f32x16 mma(u32x4 a, u32x4 b, f32x16 c) {
         return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
 }
 
+// D = A B + C on 16 x 16 x 32: lane L holds A[m = L % 16][k = 8 (L / 16) + j],
+// B[k = 8 (L / 16) + j][n = L % 16] and D[m = 4 (L / 16) + i][n = L % 16], i = 0..3.
+template <bool BF>
+__device__ __forceinline__ f32x4 mma16(u32x4 a, u32x4 b, f32x4 c) {
+    if constexpr (BF)
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+    else
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+}
+
 // Two fp32 values rounded (to nearest even) to one dword of 16-bit values.
 template <bool BF>
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
@@ -81,6 +91,33 @@ __device__ __forceinline__ u32x2 read_tr(const uint8_t *p) {
     return __builtin_bit_cast(u32x2, v);
 }
 
+// A value's maximum or sum over the two lanes L and L + 32 that share a row.
+__device__ __forceinline__ float max_halves(float x) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float sum_halves(float x) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+// The same over lanes 0-15 and 16-31, 32-47 and 48-63.
+__device__ __forceinline__ float max_quarters(float x) {
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float sum_quarters(float x) {
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+// copy16_to_lds (see dev_common.h) that the compiler may move among accesses
+// it does not depend on, between the barriers around it: the caller fills a
+// buffer that nothing reads before the next barrier.
+__device__ __forceinline__ void copy16_to_lds_free(const void *src, uint32_t lds_addr) {
+    asm volatile("global_load_lds_dwordx4 %0, off" ::"v"(src), "{m0}"(lds_addr));
+}
+
 // Workgroup barrier that waits for this wave's LDS accesses but not for its
 // global loads in flight (__syncthreads would).
 __device__ __forceinline__ void lds_barrier() {
@@ -93,6 +130,43 @@ __device__ __forceinline__ void copy_barrier() {
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
+}
+
+// Scheduling of the block they end: AHEAD LDS reads first, then READS reads
+// after every MFMAS products, so that a read is issued while the products
+// before its own are in the matrix pipe.
+template <int AHEAD>
+__device__ __forceinline__ void pipeline_begin() {
+    __builtin_amdgcn_sched_group_barrier(0x100, AHEAD, 0);
+}
+template <int LEFT, int MFMAS, int READS>
+__device__ __forceinline__ void pipeline_run() {
+    if constexpr (LEFT > 0) {
+        __builtin_amdgcn_sched_group_barrier(0x008, MFMAS, 0);
+        __builtin_amdgcn_sched_group_barrier(0x100, LEFT < READS ? LEFT : READS, 0);
+        pipeline_run<LEFT - READS, MFMAS, READS>();
+    }
+}
+// READS reads and MFMAS products in all, with VALU vector instructions of
+// other work after each product.
+template <int LEFT, int READS, int VALU>
+__device__ __forceinline__ void pipeline_mixed_run() {
+    if constexpr (LEFT > 0) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x002, VALU, 0);
+        if constexpr (READS > 0) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+        pipeline_mixed_run<LEFT - 1, READS - 1, VALU>();
+    }
+}
+template <int READS, int MFMAS, int VALU, int AHEAD>
+__device__ __forceinline__ void pipeline_mixed() {
+    __builtin_amdgcn_sched_group_barrier(0x100, AHEAD, 0);
+    pipeline_mixed_run<MFMAS, READS - AHEAD, VALU>();
+}
+template <int READS_ALL, int MFMAS, int READS, int AHEAD>
+__device__ __forceinline__ void pipeline() {
+    pipeline_begin<AHEAD>();
+    pipeline_run<READS_ALL - AHEAD, MFMAS, READS>();
 }
 
 // Stores 32 columns x 32 rows of an accumulator as 16-bit values: lane L holds

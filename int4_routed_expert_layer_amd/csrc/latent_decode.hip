@@ -5,19 +5,22 @@
 // latent ones that are key and value, 64 rotary ones that are key only):
 //   s_j = scale (q_lat . c_j + q_pe . r_j),  o = sum_j softmax(s)_j c_j,
 // so the (token, head) pairs of a sequence are rows of one product and a key
-// is read once for 64 of them.  One workgroup (four waves, one per SIMD, a CU
-// to itself) takes 64 rows and a run of 64-key tiles, with the running
-// maximum and sum of the softmax:
-//   - the tile (72 KB) is copied straight into LDS, double buffered; the copy
-//     of tile t + 1 is in flight while tile t is used;
-//   - S^T = K Q^T: wave (wm, wk) computes 32 keys x 32 rows with its rows'
-//     queries held in 144 registers, so lane L of a wave owns row L % 32;
-//   - the maxima of the two key halves and the 16-bit probabilities are
-//     exchanged through LDS;
-//   - O^T += V^T P^T: each wave computes all 64 rows of 128 latent columns
-//     (128 accumulator registers), reading V^T with transposed LDS reads.
+// is read once for 64 of them.  One workgroup of eight waves has a CU to
+// itself and takes 64 rows and a run of keys in steps of 32, with the running
+// maximum and sum of the softmax.  Each SIMD holds a wave of either kind:
+//   - a scoring wave computes S^T = K Q^T of step t, 16 keys x 32 rows, with its
+//     rows' queries in 144 registers, and writes the 16-bit probabilities to LDS;
+//   - a summing wave computes O^T += V^T P^T of step t - 1, 64 rows x 128 latent
+//     columns in 128 registers, reading V^T with transposed LDS reads, and
+//     copies the keys of step t + 2 (36 KB a step, a ring of four) from the
+//     cache straight into LDS.
+// The two meet at one barrier a step.  Between barriers each has latencies
+// that it cannot hide by itself (its first LDS reads, the exponentials, the
+// issue of the copies); the products of the other fill them.  One kind of
+// wave doing both in turn, at one wave per SIMD, took 1.37 us a step against
+// the 0.45 us of its products.
 // Splitting the keys of the first product and the columns of the second means
-// that each wave reads half of K and a quarter of V from LDS; with rows alone
+// that each wave reads half of K or a quarter of V from LDS; with rows alone
 // split every wave would read all of both.
 //
 // A sequence's keys are cut into pieces so that every CU has one (the plan);
@@ -33,26 +36,33 @@ using dev::f32x4;
 using dev::u32x2;
 using dev::u32x4;
 
+constexpr int kStepKeys = 32;
 constexpr int kBlocks = kCacheRow / 64;                  // 64-column blocks of a cached row: 8 latent, 1 rotary
 constexpr int kLatentBlocks = kLatent / 64;
-constexpr int kBlockBytes = kTileKeys * 128;
-constexpr int kTileBytes = kBlocks * kBlockBytes;        // 72 KB
-constexpr int kSteps = kCacheRow / 16;                   // K steps of the first product
-// The running maximum of a row moves only when a tile exceeds it by more than
+constexpr int kBlockBytes = kStepKeys * 128;
+constexpr int kStepBytes = kBlocks * kBlockBytes;        // 36 KB
+constexpr int kRing = 4;
+constexpr int kDepth = kCacheRow / 32;                   // K steps of the first product
+// The running maximum of a row moves only when a step exceeds it by more than
 // 2^kSlack: the accumulator is then rarely rescaled, and probabilities stay
 // below 2^kSlack, far inside the range of both 16-bit types and of the sums.
 constexpr float kSlack = 8.0f;
+constexpr int kKeyAhead = 6;                             // LDS reads in flight ahead of the products that use them
 constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.69314718055994531f;
 
-// Which 64 keys of a tile a row sees, as bits.  Rows of a chain see keys up to
+// Probabilities of a step: 64 rows of 32 keys, 64 bytes a row; the XOR spreads
+// 16 rows read at one 16-byte unit over all banks.
+__device__ __forceinline__ int weight_unit(int r, int q) { return r * 64 + ((q ^ ((r >> 2) & 3)) << 4); }
+
+// Which of the 64 keys from key0 on a row sees, as bits.  Rows of a chain see keys up to
 // their own position; rows of a tree see the context and the nodes of their
 // ancestor bits.
 __device__ __forceinline__ uint64_t below(int c) { return c >= 64 ? ~0ull : c <= 0 ? 0ull : (1ull << c) - 1; }
-__device__ __forceinline__ uint64_t seen_keys(const DecodeArgs &a, const DecodeItem &it, int node, int t) {
-    const int ctx = it.len - it.n, key0 = t * kTileKeys;
+__device__ __forceinline__ uint64_t seen_keys(const DecodeArgs &a, const DecodeItem &it, int node, int key0) {
+    const int ctx = it.len - it.n;
     if (!a.mask) return below(ctx + node + 1 - key0);
     const uint64_t *m = a.mask + static_cast<int64_t>(it.q0 + node) * a.mask_words;
-    const int d = key0 - ctx;                            // node index of the tile's first key
+    const int d = key0 - ctx;                            // node index of the first key
     uint64_t v;
     if (d <= -64) {
         v = ~0ull;
@@ -66,244 +76,389 @@ __device__ __forceinline__ uint64_t seen_keys(const DecodeArgs &a, const DecodeI
     return v & below(it.len - key0);
 }
 
+constexpr int kThreads = 512;
+
+// What both kinds of wave know of an item.
+struct Shared {
+    uint8_t *kv, *p;                   // [kRing] steps of keys; [2] steps of probabilities
+    float *red, *fac, *sum;            // [2][2][64] maxima by step parity and key half; [64]; [2][64]
+    int *raise, *bad;                  // [3] by step; one flag
+    int t0, t1, open;                  // steps; keys below `open` are seen by every row
+    __device__ uint8_t *ring(int t) const { return kv + ((t - t0) & (kRing - 1)) * kStepBytes; }
+    __device__ uint8_t *weights(int t) const { return p + (t & 1) * (kTileRows * 64); }
+    __device__ float *maxima(int t, int half) const { return red + ((t & 1) * 2 + half) * kTileRows; }
+};
+
+// In the careful pass, rows that a step hides from some are cleaned: they
+// hold what other branches left there, their weight is zero, and zero times
+// inf or NaN must not reach a row that does not see them.  (A row that sees
+// such a key has a NaN score.)
 template <bool BF>
-__global__ __launch_bounds__(256, 1) void latent_decode_kernel(DecodeArgs a) {
-    __shared__ __align__(1024) uint8_t s_kv[2 * kTileBytes];
-    __shared__ __align__(1024) uint8_t s_p[kTileRows * 128];
-    __shared__ float s_red[2][kTileRows];
-    __shared__ float s_fac[kTileRows];
-    __shared__ int s_bad;
-    const int tid = threadIdx.x, lane = tid & 63, wave = dev::wave_id();
-    const int wm = wave & 1, wk = wave >> 1;
-    const int l31 = lane & 31, lh = lane >> 5;
-    const uint32_t kv_lds = dev::lds_address(s_kv);
+__device__ __forceinline__ void clean(const Shared &sh, int t) {
+    u32x4 *v = reinterpret_cast<u32x4 *>(sh.ring(t));
+    for (int i = threadIdx.x; i < kLatentBlocks * kBlockBytes / 16; i += kThreads) {
+        u32x4 w = v[i];
+#pragma unroll
+        for (int d = 0; d < 4; ++d) w[d] &= ~dev::nonfinite_halves<BF>(w[d]);
+        v[i] = w;
+    }
+    dev::lds_barrier();
+}
+
+// The scoring waves' part of an item: wave (wm, wk) scores keys 16 wk .. + 15 of
+// each step for rows 32 wm .. + 31; lane L owns rows row and row + 16, row =
+// 32 wm + L % 16.  Leaves the running maxima in m.
+template <bool BF>
+__device__ __forceinline__ void score_item(const DecodeArgs &a, const DecodeItem &it, const Shared &sh, int rows, bool careful,
+                                           float (&m)[2]) {
+    const int lane = threadIdx.x & 63, wave = dev::wave_id();
+    const int wm = wave & 1, wk = (wave >> 1) & 1, l15 = lane & 15, lq = lane >> 4;
+    const int row = 32 * wm + l15;
     const float c = a.scale * kLog2e;
-
-    const int n_items = dev::ld_uniform(a.plan.head);
-    const int grid = static_cast<int>(gridDim.x);
-    for (int first = 0; first < n_items; first += grid) {
-        // Neighbouring items share keys: eight contiguous runs, one per XCD.
-        const int here = min(grid, n_items - first), run = (here + 7) / 8;
-        const int bx = static_cast<int>(blockIdx.x) & 7, by = static_cast<int>(blockIdx.x) >> 3;
-        if (by >= run || bx * run + by >= here) continue;
-        typedef int32_t int8v __attribute__((ext_vector_type(8)));
-        const DecodeItem it = __builtin_bit_cast(
-            DecodeItem, dev::ld_uniform(reinterpret_cast<const int8v *>(a.plan.items + first + bx * run + by)));
-        const int rows = min(kTileRows, it.n * a.n_heads - it.row0);
-        const int row = 32 * wm + l31;                   // the row this lane scores
-        const int rr = it.row0 + min(row, rows - 1);
-        const int node = rr / a.n_heads, head = rr - node * a.n_heads;
-
-        // Copies: per tile this lane fetches one 16-byte unit of each block of
-        // two keys; their page numbers are read one tile ahead.
-        const int cr = 16 * wave + (lane >> 3);
-        const int32_t *table = a.cache.table + it.seq * a.cache.table_stride;
-        bool bad_page = false;
-        auto page_of = [&](int t, int j) {
-            const int pos = min(t * kTileKeys + cr + 8 * j, it.len - 1), at = pos >> a.cache.page_shift;
-            int pg = at < a.cache.table_cols ? table[at] : -1;
-            if (pg < 0 || pg >= a.cache.n_pages) {
-                bad_page = true;
-                pg = 0;
-            }
-            return pg;
+    int node[2];
+    u32x4 q[kDepth][2];
+#pragma unroll
+    for (int rb = 0; rb < 2; ++rb) {
+        const int rr = it.row0 + min(row + 16 * rb, rows - 1);
+        node[rb] = rr / a.n_heads;
+        const int head = rr - node[rb] * a.n_heads;
+        const int64_t tok = it.q0 + node[rb];
+        const uint8_t *ql = a.q_lat + (tok * a.ql_tok + head * a.ql_head) * 2 + 16 * lq;
+        const uint8_t *qp = a.q_pe + (tok * a.qp_tok + head * a.qp_head) * 2 + 16 * lq;
+#pragma unroll
+        for (int k = 0; k < kDepth; ++k) q[k][rb] = dev::gload<u32x4>(k < kLatent / 32 ? ql + 64 * k : qp + 64 * (k - kLatent / 32));
+    }
+    m[0] = m[1] = -__builtin_inff();
+    float l[2] = {0.0f, 0.0f};
+    f32x4 s[2], s_prev[2];
+    float sum_prev[2];
+    auto score = [&](int t) {
+        const uint8_t *kr = sh.ring(t) + 16 * wk * 128;
+        auto key = [&](int k) {
+            return *reinterpret_cast<const u32x4 *>(kr + (k >> 1) * kBlockBytes + dev::tile_unit(l15, 4 * (k & 1) + lq));
         };
-        auto copy_tile = [&](int t, int buf, const int (&pg)[2]) {
+        u32x4 kf[kKeyAhead];
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int pos = min(t * kTileKeys + cr + 8 * j, it.len - 1);
-                const int in = pos & ((1 << a.cache.page_shift) - 1);
-                const uint8_t *src = a.cache.base + (pg[j] * a.cache.page_stride + static_cast<int64_t>(in) * kCacheRow) * 2 +
-                                     (((lane & 7) ^ dev::tile_swz(8 * j + (lane >> 3))) << 4);
-                const uint32_t dst = kv_lds + buf * kTileBytes + (2 * wave + j) * 1024;
+        for (int k = 0; k < kKeyAhead; ++k) kf[k] = key(k);
 #pragma unroll
-                for (int b = 0; b < kBlocks; ++b) dev::copy16_to_lds(src + b * 128, dst + b * kBlockBytes);
-            }
-        };
-
-        u32x4 q[kSteps];
-        {
-            const int64_t tok = it.q0 + node;
-            const uint8_t *ql = a.q_lat + (tok * a.ql_tok + head * a.ql_head) * 2 + 16 * lh;
-            const uint8_t *qp = a.q_pe + (tok * a.qp_tok + head * a.qp_head) * 2 + 16 * lh;
+        for (int rb = 0; rb < 2; ++rb) s[rb] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-            for (int k = 0; k < kLatent / 16; ++k) q[k] = dev::gload<u32x4>(ql + 32 * k);
+        for (int k = 0; k < kDepth; ++k) {
 #pragma unroll
-            for (int k = kLatent / 16; k < kSteps; ++k) q[k] = dev::gload<u32x4>(qp + 32 * (k - kLatent / 16));
+            for (int rb = 0; rb < 2; ++rb) s[rb] = dev::mma16<BF>(kf[k % kKeyAhead], q[k][rb], s[rb]);
+            if (k + kKeyAhead < kDepth) kf[k % kKeyAhead] = key(k + kKeyAhead);
         }
+        dev::pipeline<kDepth, 2, 1, kKeyAhead>();
+        __builtin_amdgcn_sched_barrier(0);
+        if ((t + 1) * kStepKeys > sh.open) {
+#pragma unroll
+            for (int rb = 0; rb < 2; ++rb) {
+                const uint32_t seen = static_cast<uint32_t>(seen_keys(a, it, node[rb], t * kStepKeys)) >> (16 * wk + 4 * lq);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (!((seen >> i) & 1)) s[rb][i] = -__builtin_inff();
+            }
+        }
+    };
+    auto row_max = [&](int rb) {
+        const float x = fmaxf(fmaxf(s[rb][0], s[rb][1]), fmaxf(s[rb][2], s[rb][3]));
+        return dev::max_halves(dev::max_quarters(x));
+    };
+    auto post_max = [&](int t, const float (&mx)[2]) {
+        if (lq == 0) {
+            sh.maxima(t, wk)[row] = mx[0];
+            sh.maxima(t, wk)[row + 16] = mx[1];
+        }
+    };
+    // Probabilities of scores v against the running maxima; the lane's part of
+    // the row sums.
+    auto weigh = [&](int t, const f32x4 (&v)[2], float (&sum)[2]) {
+#pragma unroll
+        for (int rb = 0; rb < 2; ++rb) {
+            const float ms = m[rb] == -__builtin_inff() ? 0.0f : m[rb];
+            float p[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(v[rb][i], c, -ms));
+            sum[rb] = (p[0] + p[1]) + (p[2] + p[3]);
+            *reinterpret_cast<u32x2 *>(sh.weights(t) + weight_unit(row + 16 * rb, 2 * wk + (lq >> 1)) + 8 * (lq & 1)) =
+                u32x2{dev::pack2<BF>(p[0], p[1]), dev::pack2<BF>(p[2], p[3])};
+        }
+    };
+    // New maxima from both key halves of step t, and the factors of what was
+    // summed before it.
+    auto take_max = [&](int t, float slack) {
+#pragma unroll
+        for (int rb = 0; rb < 2; ++rb) {
+            const int r = row + 16 * rb;
+            const float tm = fmaxf(sh.maxima(t, 0)[r], sh.maxima(t, 1)[r]) * c;
+            const float m1 = tm > m[rb] + slack ? tm : m[rb];
+            const float fac = m1 == m[rb] ? 1.0f : __builtin_amdgcn_exp2f(m[rb] - m1);
+            m[rb] = m1;
+            l[rb] *= fac;
+            if (wk == 0 && lq == 0) sh.fac[r] = fac;
+        }
+    };
+    // After the barrier behind step t: where a row exceeded its maximum by
+    // more than the slack, the step is weighed again.
+    auto settle = [&](int t) {
+        if (__builtin_amdgcn_readfirstlane(sh.raise[(t - sh.t0) % 3])) {
+            take_max(t, kSlack);
+            weigh(t, s_prev, sum_prev);
+            dev::lds_barrier();
+        }
+        l[0] += sum_prev[0];
+        l[1] += sum_prev[1];
+        if (careful && (t + 1) * kStepKeys > sh.open) clean<BF>(sh, t);
+    };
 
-        const int ctx = it.len - it.n;
-        const int open = ctx + (a.mask ? 0 : 1);         // keys below are seen by every row
-        f32x16 acc[4][2];                                // [32 columns][32 rows] blocks of O^T
-        float m, l;
-        for (int careful = 0; careful < 2; ++careful) {
+    if (sh.t0 < sh.t1) {
+        // First step: its maxima are exchanged before it is weighed.
+        dev::lds_barrier();
+        score(sh.t0);
+        const float mx[2] = {row_max(0), row_max(1)};
+        post_max(sh.t0, mx);
+        dev::lds_barrier();
+        take_max(sh.t0, 0.0f);
+        weigh(sh.t0, s, sum_prev);
+        s_prev[0] = s[0];
+        s_prev[1] = s[1];
+        for (int t = sh.t0 + 1; t < sh.t1; ++t) {
+            dev::lds_barrier();
+            settle(t - 1);
+            if (threadIdx.x == 0) sh.raise[(t + 1 - sh.t0) % 3] = 0;
+            score(t);
+            const float mx[2] = {row_max(0), row_max(1)};
+            weigh(t, s, sum_prev);
+            post_max(t, mx);
+            if (__any(mx[0] * c > m[0] + kSlack || mx[1] * c > m[1] + kSlack)) sh.raise[(t - sh.t0) % 3] = 1;
+            s_prev[0] = s[0];
+            s_prev[1] = s[1];
+        }
+        dev::lds_barrier();
+        settle(sh.t1 - 1);
+    }
+#pragma unroll
+    for (int rb = 0; rb < 2; ++rb) {
+        const float sum = dev::sum_halves(dev::sum_quarters(l[rb]));
+        if (lq == 0) sh.sum[wk * kTileRows + row + 16 * rb] = sum;
+    }
+}
+
+// The summing waves' part: wave w copies keys 8 w .. + 7 of each step and sums
+// columns 128 w .. + 127 for all rows.
+template <bool BF>
+__device__ __forceinline__ void sum_item(const DecodeArgs &a, const DecodeItem &it, const Shared &sh, uint32_t kv_lds, bool careful,
+                                         bool &bad_page, f32x16 (&acc)[4][2]) {
+    const int lane = threadIdx.x & 63, wave = dev::wave_id() & 3, l31 = lane & 31, lh = lane >> 5;
+#pragma unroll
+    for (int cb = 0; cb < 4; ++cb)
+#pragma unroll
+        for (int rb = 0; rb < 2; ++rb)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) acc[cb][rb][i] = 0.0f;
+    if (sh.t0 >= sh.t1) return;
+    // Each lane copies one 16-byte unit of every block of one key.  Pages of
+    // eight rows or more hold all of a wave's keys: the page number is then the
+    // wave's, read by the scalar unit a step ahead (a vector load in flight
+    // would make its use wait for the copies issued before it).
+    const int cr = 8 * wave + (lane >> 3);
+    const int cu = ((lane & 7) ^ dev::tile_swz(cr)) << 4;
+    const int32_t *table = a.cache.table + it.seq * a.cache.table_stride;
+    const int shift = a.cache.page_shift, cols = a.cache.table_cols, last = sh.t1 - 1;
+    const bool wide = shift >= 3;
+    auto page_of = [&](int t) {
+        const int pos = min(min(t, last) * kStepKeys + 8 * wave, it.len - 1);
+        return dev::ld_uniform(table + min(pos >> shift, max(cols, 1) - 1));
+    };
+    const uint8_t *src;
+    uint32_t dst;
+    auto aim = [&](int t, int wave_page) {
+        t = min(t, last);                                // past the end the last step is copied again
+        const int pos = min(t * kStepKeys + cr, it.len - 1), at = pos >> shift;
+        int page = wide ? wave_page : table[min(at, max(cols, 1) - 1)];
+        if (page < 0 || page >= a.cache.n_pages || at >= cols) {
+            bad_page = true;
+            page = 0;
+        }
+        src = a.cache.base + (page * a.cache.page_stride + static_cast<int64_t>(pos & ((1 << shift) - 1)) * kCacheRow) * 2 + cu;
+        dst = kv_lds + ((t - sh.t0) & (kRing - 1)) * kStepBytes + wave * 1024;
+    };
+    auto copy = [&](int b0, int b1) {
+#pragma unroll
+        for (int b = b0; b < b1; ++b) dev::copy16_to_lds(src + b * 128, dst + b * kBlockBytes);
+    };
+    // Rows' factors where the maxima moved, and the careful pass.
+    auto settle = [&](int t) {
+        if (__builtin_amdgcn_readfirstlane(sh.raise[(t - sh.t0) % 3])) {
+            dev::lds_barrier();
+            const float f0 = sh.fac[l31], f1 = sh.fac[32 + l31];
 #pragma unroll
             for (int cb = 0; cb < 4; ++cb)
 #pragma unroll
-                for (int rb = 0; rb < 2; ++rb)
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) acc[cb][rb][i] = 0.0f;
-            m = -__builtin_inff();
-            l = 0.0f;
-            dev::lds_barrier();                          // the buffers of the item (or pass) before are free
-            if (tid == 0) s_bad = 0;
-            int pg[2] = {0, 0};
-            if (it.t0 < it.t1) {
-                const int now[2] = {page_of(it.t0, 0), page_of(it.t0, 1)};
-                copy_tile(it.t0, 0, now);
-                if (it.t0 + 1 < it.t1) {
-                    pg[0] = page_of(it.t0 + 1, 0);
-                    pg[1] = page_of(it.t0 + 1, 1);
+                for (int i = 0; i < 16; ++i) {
+                    acc[cb][0][i] *= f0;
+                    acc[cb][1][i] *= f1;
                 }
-            }
-            for (int t = it.t0; t < it.t1; ++t) {
-                const int buf = (t - it.t0) & 1;
-                uint8_t *kv = s_kv + buf * kTileBytes;
-                dev::copy_barrier();
-                if (t + 1 < it.t1) {
-                    copy_tile(t + 1, buf ^ 1, pg);
-                    if (t + 2 < it.t1) {
-                        pg[0] = page_of(t + 2, 0);
-                        pg[1] = page_of(t + 2, 1);
-                    }
-                }
-                // S^T of 32 keys (wk) x 32 rows (wm), in two chains.
-                f32x16 s0, s1;
-#pragma unroll
-                for (int i = 0; i < 16; ++i) s0[i] = s1[i] = 0.0f;
-                const uint8_t *kr = kv + 32 * wk * 128;
-#pragma unroll
-                for (int k = 0; k < kSteps; k += 2) {
-                    const uint8_t *blk = kr + (k >> 2) * kBlockBytes;
-                    const u32x4 k0 = *reinterpret_cast<const u32x4 *>(blk + dev::tile_unit(l31, 2 * (k & 3) + lh));
-                    const u32x4 k1 = *reinterpret_cast<const u32x4 *>(blk + dev::tile_unit(l31, 2 * ((k + 1) & 3) + lh));
-                    s0 = dev::mma<BF>(k0, q[k], s0);
-                    s1 = dev::mma<BF>(k1, q[k + 1], s1);
-                }
-                const bool masked = (t + 1) * kTileKeys > open;
-#pragma unroll
-                for (int i = 0; i < 16; ++i) s0[i] += s1[i];
-                if (masked) {
-                    const uint64_t seen = seen_keys(a, it, node, t) >> (32 * wk + 4 * lh);
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        if (!((seen >> (8 * (i >> 2) + (i & 3))) & 1)) s0[i] = -__builtin_inff();
-                }
-                float mx = s0[0];
-#pragma unroll
-                for (int i = 1; i < 16; ++i) mx = fmaxf(mx, s0[i]);
-                mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
-                if (lh == 0) s_red[wk][row] = mx;
-                dev::lds_barrier();
-                const float tm = fmaxf(mx, s_red[wk ^ 1][row]) * c;
-                const float m1 = tm > m + kSlack ? tm : m;
-                const float fac = m1 == m ? 1.0f : __builtin_amdgcn_exp2f(m - m1);
-                m = m1;
-                const float ms = m1 == -__builtin_inff() ? 0.0f : m1;
-                float sum = 0.0f;
-#pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    float p[4];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        p[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(s0[4 * g + j], c, -ms));
-                        sum += p[j];
-                    }
-                    *reinterpret_cast<u32x2 *>(s_p + dev::tile_unit(row, 4 * wk + g) + 8 * lh) =
-                        u32x2{dev::pack2<BF>(p[0], p[1]), dev::pack2<BF>(p[2], p[3])};
-                }
-                l = l * fac + sum;
-                if (wk == 0 && lh == 0) s_fac[row] = fac;
-                if (careful && masked) {
-                    // Rows a tile hides hold what other branches left there:
-                    // their weight is zero, and zero times inf or NaN must not
-                    // reach this row.  (A row that sees such a key already has
-                    // a NaN score.)
-                    u32x4 *v = reinterpret_cast<u32x4 *>(kv);
-                    for (int i = tid; i < kLatentBlocks * kBlockBytes / 16; i += 256) {
-                        u32x4 w = v[i];
-#pragma unroll
-                        for (int d = 0; d < 4; ++d) w[d] &= ~dev::nonfinite_halves<BF>(w[d]);
-                        v[i] = w;
-                    }
-                }
-                dev::lds_barrier();
-                const float f0 = s_fac[l31], f1 = s_fac[32 + l31];
-                if (__any(f0 != 1.0f || f1 != 1.0f)) {
-#pragma unroll
-                    for (int cb = 0; cb < 4; ++cb)
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            acc[cb][0][i] *= f0;
-                            acc[cb][1][i] *= f1;
-                        }
-                }
-                // O^T: columns 128 wave .. + 127, 16 keys per step.
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const u32x4 p0 = *reinterpret_cast<const u32x4 *>(s_p + dev::tile_unit(l31, 2 * k + lh));
-                    const u32x4 p1 = *reinterpret_cast<const u32x4 *>(s_p + dev::tile_unit(32 + l31, 2 * k + lh));
-#pragma unroll
-                    for (int cb = 0; cb < 4; ++cb) {
-                        const uint8_t *blk = kv + (2 * wave + (cb >> 1)) * kBlockBytes + 16 * k * 128;
-                        const int unit = 4 * (cb & 1) + 2 * ((lane >> 4) & 1) + ((lane >> 1) & 1);
-                        const int kr0 = 8 * lh + ((lane >> 2) & 3);
-                        const u32x2 a0 = dev::read_tr(blk + dev::tile_unit(kr0, unit) + 8 * (lane & 1));
-                        const u32x2 a1 = dev::read_tr(blk + dev::tile_unit(kr0 + 4, unit) + 8 * (lane & 1));
-                        const u32x4 v = {a0[0], a0[1], a1[0], a1[1]};
-                        acc[cb][0] = dev::mma<BF>(v, p0, acc[cb][0]);
-                        acc[cb][1] = dev::mma<BF>(v, p1, acc[cb][1]);
-                    }
-                }
-            }
-            // The row sums of both key halves; whether anything is not finite.
-            l += __shfl_xor(l, 32, 64);
-            dev::lds_barrier();
-            if (lh == 0) s_red[wk][row] = l;
-            float z = 0.0f;
-#pragma unroll
-            for (int cb = 0; cb < 4; ++cb)
-#pragma unroll
-                for (int rb = 0; rb < 2; ++rb)
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) z = __builtin_fmaf(acc[cb][rb][i], 0.0f, z);
-            if (__any(z != 0.0f)) s_bad = 1;
-            dev::lds_barrier();
-            if (!(s_bad && it.t1 * kTileKeys > open)) break;
         }
-
-        const float l0 = s_red[0][l31] + s_red[1][l31], l1 = s_red[0][32 + l31] + s_red[1][32 + l31];
-        const int64_t out_row = static_cast<int64_t>(it.q0) * a.n_heads + it.row0;
-        if (it.slot < 0) {
-            const float i0 = l0 == 0.0f ? 0.0f : 1.0f / l0, i1 = l1 == 0.0f ? 0.0f : 1.0f / l1;
+        if (careful && (t + 1) * kStepKeys > sh.open) clean<BF>(sh, t);
+    };
+    const int kr0 = 8 * lh + ((lane >> 2) & 3);
+    auto add_values = [&](int t, bool more) {
+        const uint8_t *vr = sh.ring(t) + 2 * wave * kBlockBytes + 8 * (lane & 1);
+        const uint8_t *pr = sh.weights(t);
+        u32x4 pf[2][2], vf[2][4];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+#pragma unroll
+            for (int rb = 0; rb < 2; ++rb) pf[k][rb] = *reinterpret_cast<const u32x4 *>(pr + weight_unit(32 * rb + l31, 2 * k + lh));
 #pragma unroll
             for (int cb = 0; cb < 4; ++cb) {
-                const int col = 128 * wave + 32 * cb;
-                uint8_t *o = a.out + ((out_row + l31) * kLatent + col) * 2;
-                dev::store_tile16<BF>(acc[cb][0], i0, l31 < rows ? o : nullptr);
-                dev::store_tile16<BF>(acc[cb][1], i1, 32 + l31 < rows ? o + 32 * kLatent * 2 : nullptr);
+                const uint8_t *blk = vr + (cb >> 1) * kBlockBytes + 16 * k * 128;
+                const int unit = 4 * (cb & 1) + 2 * ((lane >> 4) & 1) + ((lane >> 1) & 1);
+                const u32x2 a0 = dev::read_tr(blk + dev::tile_unit(kr0, unit));
+                const u32x2 a1 = dev::read_tr(blk + dev::tile_unit(kr0 + 4, unit));
+                vf[k][cb] = u32x4{a0[0], a0[1], a1[0], a1[1]};
             }
-            if (a.lse && wk == 0 && lh == 0 && row < rows) {
-                const float lr = wm ? l1 : l0;
-                a.lse[out_row + row] = lr == 0.0f ? -__builtin_inff() : (m + __builtin_amdgcn_logf(lr)) * kLn2;
-            }
-        } else {
-            float *part = a.part + static_cast<int64_t>(it.slot) * kTileRows * kLatent;
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
 #pragma unroll
             for (int cb = 0; cb < 4; ++cb)
 #pragma unroll
-                for (int rb = 0; rb < 2; ++rb)
-                    if (32 * rb + l31 < rows) {
-                        float *o = part + (32 * rb + l31) * kLatent + 128 * wave + 32 * cb + 4 * lh;
+                for (int rb = 0; rb < 2; ++rb) acc[cb][rb] = dev::mma<BF>(vf[k][cb], pf[k][rb], acc[cb][rb]);
+        __builtin_amdgcn_sched_barrier(0);
+        if (more) copy(0, kBlocks);
+    };
+
+    const int pg0 = page_of(sh.t0), pg1 = page_of(sh.t0 + 1);
+    int page = page_of(sh.t0 + 2);
+    aim(sh.t0, pg0);
+    copy(0, kBlocks);
+    aim(sh.t0 + 1, pg1);
+    copy(0, kBlocks);
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kBlocks) : "memory");
+    dev::lds_barrier();                                  // step t0 has landed
+    aim(sh.t0 + 2, page);
+    copy(0, kBlocks);
+    page = page_of(sh.t0 + 3);
+    dev::lds_barrier();                                  // the first maxima
+    for (int t = sh.t0 + 1; t < sh.t1; ++t) {
+        // Step t has landed when only the copies of step t + 1 are in flight.
+        asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kBlocks) : "memory");
+        dev::lds_barrier();
+        aim(t + 2, page);
+        page = page_of(t + 3);
+        settle(t - 1);
+        add_values(t - 1, true);
+    }
+    dev::copy_barrier();
+    settle(last);
+    add_values(last, false);
+    float z = 0.0f;
 #pragma unroll
-                        for (int g = 0; g < 4; ++g)
-                            *reinterpret_cast<f32x4 *>(o + 8 * g) = f32x4{acc[cb][rb][4 * g], acc[cb][rb][4 * g + 1],
-                                                                          acc[cb][rb][4 * g + 2], acc[cb][rb][4 * g + 3]};
+    for (int cb = 0; cb < 4; ++cb)
+#pragma unroll
+        for (int rb = 0; rb < 2; ++rb)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) z = __builtin_fmaf(acc[cb][rb][i], 0.0f, z);
+    if (__any(z != 0.0f)) *sh.bad = 1;
+}
+
+// This workgroup's item of the round that starts at item `first`, and its
+// steps; false where it has none.  Neighbouring items share keys: a round's
+// items lie in eight contiguous runs, one per XCD.
+__device__ __forceinline__ bool take_item(const DecodeArgs &a, int first, int n_items, DecodeItem &it, Shared &sh) {
+    const int here = min(static_cast<int>(gridDim.x), n_items - first), run = (here + 7) / 8;
+    const int bx = static_cast<int>(blockIdx.x) & 7, by = static_cast<int>(blockIdx.x) >> 3;
+    if (by >= run || bx * run + by >= here) return false;
+    typedef int32_t int8v __attribute__((ext_vector_type(8)));
+    it = __builtin_bit_cast(DecodeItem, dev::ld_uniform(reinterpret_cast<const int8v *>(a.plan.items + first + bx * run + by)));
+    sh.t0 = 2 * it.t0;
+    sh.t1 = min(2 * it.t1, (it.len + kStepKeys - 1) / kStepKeys);
+    sh.open = it.len - it.n + (a.mask ? 0 : 1);
+    return true;
+}
+
+template <bool BF>
+__global__ __launch_bounds__(kThreads, 2) void latent_decode_kernel(DecodeArgs a) {
+    __shared__ __align__(1024) uint8_t s_kv[kRing * kStepBytes];
+    __shared__ __align__(1024) uint8_t s_p[2 * kTileRows * 64];
+    __shared__ float s_red[2 * 2 * kTileRows], s_fac[kTileRows], s_sum[2 * kTileRows];
+    __shared__ int s_raise[3], s_bad;
+    const int tid = threadIdx.x, lane = tid & 63, wave = dev::wave_id();
+    const int l31 = lane & 31, lh = lane >> 5;
+    const uint32_t kv_lds = dev::lds_address(s_kv);
+
+    // The two kinds walk the items in loops of their own (and meet at the same
+    // barriers): neither then holds registers for the other.
+    const int n_items = dev::ld_uniform(a.plan.head);
+    Shared sh{s_kv, s_p, s_red, s_fac, s_sum, s_raise, &s_bad, 0, 0, 0};
+    if (wave < 4) {
+        for (int first = 0; first < n_items; first += static_cast<int>(gridDim.x)) {
+            DecodeItem it;
+            if (!take_item(a, first, n_items, it, sh)) continue;
+            const int rows = min(kTileRows, it.n * a.n_heads - it.row0);
+            float m[2];
+            for (int careful = 0; careful < 2; ++careful) {
+                dev::lds_barrier();                      // the buffers of the item (or pass) before are free
+                if (tid == 0) s_bad = s_raise[0] = s_raise[1] = s_raise[2] = 0;
+                score_item<BF>(a, it, sh, rows, careful, m);
+                dev::lds_barrier();
+                if (!(s_bad && sh.t1 * kStepKeys > sh.open)) break;
+            }
+            if ((wave >> 1) == 0 && lane < 16)
+#pragma unroll
+                for (int rb = 0; rb < 2; ++rb) {
+                    const int r = 32 * wave + lane + 16 * rb;
+                    if (r >= rows) continue;
+                    const float lr = s_sum[r] + s_sum[kTileRows + r];
+                    if (it.slot >= 0) {
+                        float *ml = a.part_ml + (static_cast<int64_t>(it.slot) * kTileRows + r) * 2;
+                        ml[0] = m[rb];
+                        ml[1] = lr;
+                    } else if (a.lse) {
+                        a.lse[static_cast<int64_t>(it.q0) * a.n_heads + it.row0 + r] =
+                            lr == 0.0f ? -__builtin_inff() : (m[rb] + __builtin_amdgcn_logf(lr)) * kLn2;
                     }
-            if (wk == 0 && lh == 0 && row < rows) {
-                float *ml = a.part_ml + (static_cast<int64_t>(it.slot) * kTileRows + row) * 2;
-                ml[0] = m;
-                ml[1] = wm ? l1 : l0;
+                }
+        }
+    } else {
+        const int w = wave - 4;
+        bool bad_page = false;
+        for (int first = 0; first < n_items; first += static_cast<int>(gridDim.x)) {
+            DecodeItem it;
+            if (!take_item(a, first, n_items, it, sh)) continue;
+            const int rows = min(kTileRows, it.n * a.n_heads - it.row0);
+            f32x16 acc[4][2];                            // [32 columns][32 rows] blocks of O^T
+            for (int careful = 0; careful < 2; ++careful) {
+                dev::lds_barrier();
+                sum_item<BF>(a, it, sh, kv_lds, careful, bad_page, acc);
+                dev::lds_barrier();
+                if (!(s_bad && sh.t1 * kStepKeys > sh.open)) break;
+            }
+            if (it.slot < 0) {
+                const int64_t out_row = static_cast<int64_t>(it.q0) * a.n_heads + it.row0;
+                const float l0 = s_sum[l31] + s_sum[kTileRows + l31], l1 = s_sum[32 + l31] + s_sum[kTileRows + 32 + l31];
+                const float i0 = l0 == 0.0f ? 0.0f : 1.0f / l0, i1 = l1 == 0.0f ? 0.0f : 1.0f / l1;
+#pragma unroll
+                for (int cb = 0; cb < 4; ++cb) {
+                    uint8_t *o = a.out + ((out_row + l31) * kLatent + 128 * w + 32 * cb) * 2;
+                    dev::store_tile16<BF>(acc[cb][0], i0, l31 < rows ? o : nullptr);
+                    dev::store_tile16<BF>(acc[cb][1], i1, 32 + l31 < rows ? o + 32 * kLatent * 2 : nullptr);
+                }
+            } else {
+                float *part = a.part + static_cast<int64_t>(it.slot) * kTileRows * kLatent;
+#pragma unroll
+                for (int cb = 0; cb < 4; ++cb)
+#pragma unroll
+                    for (int rb = 0; rb < 2; ++rb)
+                        if (32 * rb + l31 < rows) {
+                            float *o = part + (32 * rb + l31) * kLatent + 128 * w + 32 * cb + 4 * lh;
+#pragma unroll
+                            for (int g = 0; g < 4; ++g)
+                                *reinterpret_cast<f32x4 *>(o + 8 * g) = f32x4{acc[cb][rb][4 * g], acc[cb][rb][4 * g + 1],
+                                                                              acc[cb][rb][4 * g + 2], acc[cb][rb][4 * g + 3]};
+                        }
             }
         }
         dev::flag_if(bad_page, a.err, kErrPage);
@@ -311,12 +466,14 @@ __global__ __launch_bounds__(256, 1) void latent_decode_kernel(DecodeArgs a) {
 }
 
 // Joins the pieces of a row: with M = max m_i, o = sum 2^(m_i - M) O_i / sum
-// 2^(m_i - M) l_i.  Two rows per 256-thread workgroup, four columns per
-// thread; the pieces of one row are read in a fixed order.
+// 2^(m_i - M) l_i.  Two rows per 256-thread workgroup, two waves a row, four
+// columns per thread.  Each lane of a wave holds one piece's factor, so the
+// statistics are one load and the partial rows are all in flight together;
+// pieces are summed in a fixed order.
 template <bool BF>
 __global__ __launch_bounds__(256) void join_kernel(DecodeArgs a) {
     const int n = dev::ld_uniform(a.plan.head + 1) * (kTileRows / 2);
-    const int half = threadIdx.x >> 7, col = 4 * (threadIdx.x & 127);
+    const int lane = threadIdx.x & 63, half = dev::wave_id() >> 1, col = 4 * (threadIdx.x & 127);
     for (int w = blockIdx.x; w < n; w += gridDim.x) {
         const JoinUnit u = a.plan.joins[w / (kTileRows / 2)];
         const int r = 2 * (w % (kTileRows / 2)) + half;
@@ -324,17 +481,27 @@ __global__ __launch_bounds__(256) void join_kernel(DecodeArgs a) {
         const float *ml = a.part_ml + (static_cast<int64_t>(u.slot0) * kTileRows + r) * 2;
         const float *part = a.part + (static_cast<int64_t>(u.slot0) * kTileRows + r) * kLatent + col;
         float top = -__builtin_inff();
-        for (int i = 0; i < u.split; ++i) top = fmaxf(top, ml[i * kTileRows * 2]);
+        for (int i = lane; i < u.split; i += 64) top = fmaxf(top, ml[i * kTileRows * 2]);
+#pragma unroll
+        for (int o = 32; o; o >>= 1) top = fmaxf(top, __shfl_xor(top, o, 64));
         const float ms = top == -__builtin_inff() ? 0.0f : top;
         float l = 0.0f;
         f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 4
-        for (int i = 0; i < u.split; ++i) {
-            const float f = __builtin_amdgcn_exp2f(ml[i * kTileRows * 2] - ms);
-            const f32x4 v = *reinterpret_cast<const f32x4 *>(part + static_cast<int64_t>(i) * kTileRows * kLatent);
-            l = __builtin_fmaf(f, ml[i * kTileRows * 2 + 1], l);
+        for (int i0 = 0; i0 < u.split; i0 += 64) {
+            const int here = min(64, u.split - i0);
+            const float *mine = ml + static_cast<int64_t>(i0 + min(lane, here - 1)) * kTileRows * 2;
+            const float f = lane < here ? __builtin_amdgcn_exp2f(mine[0] - ms) : 0.0f;
+            float sum = lane < here ? f * mine[1] : 0.0f;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) o[j] = __builtin_fmaf(f, v[j], o[j]);
+            for (int d = 32; d; d >>= 1) sum += __shfl_xor(sum, d, 64);
+            l += sum;
+#pragma unroll 8
+            for (int i = 0; i < here; ++i) {
+                const float fi = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(f), i));
+                const f32x4 v = *reinterpret_cast<const f32x4 *>(part + static_cast<int64_t>(i0 + i) * kTileRows * kLatent);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) o[j] = __builtin_fmaf(fi, v[j], o[j]);
+            }
         }
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
         const int64_t row = u.out_row + r;
@@ -347,11 +514,12 @@ __global__ __launch_bounds__(256) void join_kernel(DecodeArgs a) {
 // The plan of a step, by one workgroup: each sequence's rows are cut into
 // 64-row units and its key tiles into runs of at most `per`, the run length
 // with the shortest estimated time: for one to four rounds over the CUs the
-// smallest run length that fits that many rounds, at (per + kItemCost) per
-// round.  With more units than four rounds hold, only units longer than a
+// smallest run length that fits that many rounds, at (per + kItemCost) tiles per
+// round, and the joining of the pieces.  With more units than four rounds hold, only units longer than a
 // CU's fair share are cut.
 constexpr int kPlanThreads = 1024;
 constexpr int kItemCost = 3;    // tiles: the queries, the first tile's latency and the partial result
+constexpr int kJoinItems = 64;  // pieces whose joining costs as much as a tile
 constexpr int kMinRun = 2;
 
 __device__ __forceinline__ int cut(int tiles, int per) { return max(1, (tiles + per - 1) / per); }
@@ -415,7 +583,8 @@ __global__ __launch_bounds__(kPlanThreads) void decode_plan_kernel(DecodePlan p,
             lo = w == 0 ? lo : min(lo + step * (w - 1) + 1, top);
             hi = top;
         }
-        const long long cost = static_cast<long long>(r) * (hi + kItemCost);
+        const long long items = static_cast<long long>(items_at(hi));
+        const long long cost = static_cast<long long>(r) * (hi + kItemCost) * kJoinItems + (items > static_cast<long long>(units) ? items : 0);
         if (best == 0 || cost < best_cost) {
             best = hi;
             best_cost = cost;
@@ -485,7 +654,7 @@ hipError_t launch_decode_plan(const DecodePlan &p, const int32_t *q_start, const
 }
 
 hipError_t launch_latent_decode(const DecodeArgs &a, bool bf16, int n_cu, hipStream_t s) {
-    launch(bf16 ? latent_decode_kernel<true> : latent_decode_kernel<false>, static_cast<unsigned>(n_cu), 256u, 0, s, a);
+    launch(bf16 ? latent_decode_kernel<true> : latent_decode_kernel<false>, static_cast<unsigned>(n_cu), kThreads, 0, s, a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     launch(bf16 ? join_kernel<true> : join_kernel<false>, static_cast<unsigned>(2 * n_cu), 256u, 0, s, a);

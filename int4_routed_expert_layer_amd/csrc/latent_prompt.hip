@@ -165,7 +165,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void latent_prompt_kernel(PromptArg
             for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
                 for (int i = 0; i < 16; ++i) mx = fmaxf(mx, s[kb][i]);
-            mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
+            mx = dev::max_halves(mx);
             const float tm = mx * c;
             const float m1 = tm > m + kSlack ? tm : m;
             if (__any(m1 != m)) {
@@ -246,7 +246,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void latent_prompt_kernel(PromptArg
         if (!s_bad) break;
     }
 
-    l += __shfl_xor(l, 32, 64);
+    l = dev::sum_halves(l);
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
     const int64_t out_row = static_cast<int64_t>(q0 + row0 + row) * a.n_heads + head;
     uint8_t *o = row < rows ? a.out + out_row * V * 2 : nullptr;

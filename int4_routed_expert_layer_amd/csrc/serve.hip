@@ -107,8 +107,9 @@ CacheView view(const coli_serve *S, const void *cache, int64_t page_stride, int3
     v.page_stride = page_stride;
     v.n_pages = n_pages;
     v.page_shift = __builtin_ctz(static_cast<unsigned>(S->d.page_size));
-    v.table = table;
-    v.table_stride = table_stride;
+    // A table without columns: some address that can be read; every page is out of range.
+    v.table = table_cols > 0 ? table : S->err;
+    v.table_stride = table_cols > 0 ? table_stride : 0;
     v.table_cols = table_cols;
     return v;
 }
