@@ -128,6 +128,7 @@ __device__ __forceinline__ void score_item(const DecodeArgs &a, const DecodeItem
 #pragma unroll
         for (int k = 0; k < kDepth; ++k) q[k][rb] = dev::gload<u32x4>(k < kLatent / 32 ? ql + 64 * k : qp + 64 * (k - kLatent / 32));
     }
+    __builtin_amdgcn_s_setprio(2);   // the step waits for these waves: the summing ones fill what they leave
     m[0] = m[1] = -__builtin_inff();
     float l[2] = {0.0f, 0.0f};
     f32x4 s[2], s_prev[2];
@@ -160,14 +161,22 @@ __device__ __forceinline__ void score_item(const DecodeArgs &a, const DecodeItem
             }
         }
     };
-    auto row_max = [&](int rb) {
-        const float x = fmaxf(fmaxf(s[rb][0], s[rb][1]), fmaxf(s[rb][2], s[rb][3]));
-        return dev::max_halves(dev::max_quarters(x));
+    // What the fast path needs of the running maxima: the score that calls for
+    // a new one, and the exponent's offset.
+    float limit[2], offset[2];
+    auto set_limits = [&]() {
+#pragma unroll
+        for (int rb = 0; rb < 2; ++rb) {
+            limit[rb] = (m[rb] + kSlack) / c;
+            offset[rb] = m[rb] == -__builtin_inff() ? 0.0f : -m[rb];
+        }
     };
-    auto post_max = [&](int t, const float (&mx)[2]) {
-        if (lq == 0) {
-            sh.maxima(t, wk)[row] = mx[0];
-            sh.maxima(t, wk)[row + 16] = mx[1];
+    auto lane_max = [&](const f32x4 &v) { return fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])); };
+    auto post_max = [&](int t, const f32x4 (&v)[2]) {
+#pragma unroll
+        for (int rb = 0; rb < 2; ++rb) {
+            const float x = dev::max_halves(dev::max_quarters(lane_max(v[rb])));
+            if (lq == 0) sh.maxima(t, wk)[row + 16 * rb] = x;
         }
     };
     // Probabilities of scores v against the running maxima; the lane's part of
@@ -175,10 +184,9 @@ __device__ __forceinline__ void score_item(const DecodeArgs &a, const DecodeItem
     auto weigh = [&](int t, const f32x4 (&v)[2], float (&sum)[2]) {
 #pragma unroll
         for (int rb = 0; rb < 2; ++rb) {
-            const float ms = m[rb] == -__builtin_inff() ? 0.0f : m[rb];
             float p[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(v[rb][i], c, -ms));
+            for (int i = 0; i < 4; ++i) p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(v[rb][i], c, offset[rb]));
             sum[rb] = (p[0] + p[1]) + (p[2] + p[3]);
             *reinterpret_cast<u32x2 *>(sh.weights(t) + weight_unit(row + 16 * rb, 2 * wk + (lq >> 1)) + 8 * (lq & 1)) =
                 u32x2{dev::pack2<BF>(p[0], p[1]), dev::pack2<BF>(p[2], p[3])};
@@ -197,11 +205,15 @@ __device__ __forceinline__ void score_item(const DecodeArgs &a, const DecodeItem
             l[rb] *= fac;
             if (wk == 0 && lq == 0) sh.fac[r] = fac;
         }
+        set_limits();
     };
     // After the barrier behind step t: where a row exceeded its maximum by
-    // more than the slack, the step is weighed again.
-    auto settle = [&](int t) {
-        if (__builtin_amdgcn_readfirstlane(sh.raise[(t - sh.t0) % 3])) {
+    // more than the slack, the maxima are exchanged and the step is weighed
+    // again.
+    auto settle = [&](int t, int raise) {
+        if (__builtin_amdgcn_readfirstlane(raise)) {
+            post_max(t, s_prev);
+            dev::lds_barrier();
             take_max(t, kSlack);
             weigh(t, s_prev, sum_prev);
             dev::lds_barrier();
@@ -215,8 +227,7 @@ __device__ __forceinline__ void score_item(const DecodeArgs &a, const DecodeItem
         // First step: its maxima are exchanged before it is weighed.
         dev::lds_barrier();
         score(sh.t0);
-        const float mx[2] = {row_max(0), row_max(1)};
-        post_max(sh.t0, mx);
+        post_max(sh.t0, s);
         dev::lds_barrier();
         take_max(sh.t0, 0.0f);
         weigh(sh.t0, s, sum_prev);
@@ -224,18 +235,17 @@ __device__ __forceinline__ void score_item(const DecodeArgs &a, const DecodeItem
         s_prev[1] = s[1];
         for (int t = sh.t0 + 1; t < sh.t1; ++t) {
             dev::lds_barrier();
-            settle(t - 1);
+            const int raise = sh.raise[(t - 1 - sh.t0) % 3];
             if (threadIdx.x == 0) sh.raise[(t + 1 - sh.t0) % 3] = 0;
             score(t);
-            const float mx[2] = {row_max(0), row_max(1)};
+            settle(t - 1, raise);
             weigh(t, s, sum_prev);
-            post_max(t, mx);
-            if (__any(mx[0] * c > m[0] + kSlack || mx[1] * c > m[1] + kSlack)) sh.raise[(t - sh.t0) % 3] = 1;
+            if (__any(lane_max(s[0]) > limit[0] || lane_max(s[1]) > limit[1])) sh.raise[(t - sh.t0) % 3] = 1;
             s_prev[0] = s[0];
             s_prev[1] = s[1];
         }
         dev::lds_barrier();
-        settle(sh.t1 - 1);
+        settle(sh.t1 - 1, sh.raise[(sh.t1 - 1 - sh.t0) % 3]);
     }
 #pragma unroll
     for (int rb = 0; rb < 2; ++rb) {
@@ -270,27 +280,65 @@ __device__ __forceinline__ void sum_item(const DecodeArgs &a, const DecodeItem &
         const int pos = min(min(t, last) * kStepKeys + 8 * wave, it.len - 1);
         return dev::ld_uniform(table + min(pos >> shift, max(cols, 1) - 1));
     };
-    const uint8_t *src;
-    uint32_t dst;
+    struct Copy {
+        const uint8_t *src;
+        uint32_t dst;
+    };
     auto aim = [&](int t, int wave_page) {
         t = min(t, last);                                // past the end the last step is copied again
         const int pos = min(t * kStepKeys + cr, it.len - 1), at = pos >> shift;
-        int page = wide ? wave_page : table[min(at, max(cols, 1) - 1)];
+        int page = wave_page;
+        if (!wide) {
+            page = table[min(at, max(cols, 1) - 1)];
+            asm volatile("" : "+v"(page));               // waited for here, not (with the copies) where the paths join
+        }
         if (page < 0 || page >= a.cache.n_pages || at >= cols) {
             bad_page = true;
             page = 0;
         }
-        src = a.cache.base + (page * a.cache.page_stride + static_cast<int64_t>(pos & ((1 << shift) - 1)) * kCacheRow) * 2 + cu;
-        dst = kv_lds + ((t - sh.t0) & (kRing - 1)) * kStepBytes + wave * 1024;
+        return Copy{a.cache.base + (page * a.cache.page_stride + static_cast<int64_t>(pos & ((1 << shift) - 1)) * kCacheRow) * 2 + cu,
+                    kv_lds + ((t - sh.t0) & (kRing - 1)) * kStepBytes + wave * 1024};
     };
-    auto copy = [&](int b0, int b1) {
+    auto copy = [&](const Copy &x, int b) { dev::copy16_to_lds_free(x.src + b * 128, x.dst + b * kBlockBytes); };
+    auto copy_all = [&](const Copy &x) {
 #pragma unroll
-        for (int b = b0; b < b1; ++b) dev::copy16_to_lds(src + b * 128, dst + b * kBlockBytes);
+        for (int b = 0; b < kBlocks; ++b) copy(x, b);
     };
-    // Rows' factors where the maxima moved, and the careful pass.
-    auto settle = [&](int t) {
-        if (__builtin_amdgcn_readfirstlane(sh.raise[(t - sh.t0) % 3])) {
-            dev::lds_barrier();
+    // Sums step t.  In the loop the copies `now` (of step t + 3) are issued
+    // between the products, and what the next ones need is computed there: four
+    // waves' copies keep the CU's address unit busy for about 900 clocks, nearly
+    // as long as both kinds' products take.
+    const int kr0 = 8 * lh + ((lane >> 2) & 3);
+    auto step = [&](int t, bool more, Copy &now, int &page) {
+        const int raise = sh.raise[(t - sh.t0) % 3];
+        const uint8_t *vr = sh.ring(t) + 2 * wave * kBlockBytes + 8 * (lane & 1);
+        const uint8_t *pr = sh.weights(t);
+        u32x4 pf[2][2], vf[2][4];
+        auto read_weights = [&]() {
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+                for (int rb = 0; rb < 2; ++rb) pf[k][rb] = *reinterpret_cast<const u32x4 *>(pr + weight_unit(32 * rb + l31, 2 * k + lh));
+        };
+        auto read_values = [&]() {
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+                for (int cb = 0; cb < 4; ++cb) {
+                    const uint8_t *blk = vr + (cb >> 1) * kBlockBytes + 16 * k * 128;
+                    const int unit = 4 * (cb & 1) + 2 * ((lane >> 4) & 1) + ((lane >> 1) & 1);
+                    const u32x2 a0 = dev::read_tr(blk + dev::tile_unit(kr0, unit));
+                    const u32x2 a1 = dev::read_tr(blk + dev::tile_unit(kr0 + 4, unit));
+                    vf[k][cb] = u32x4{a0[0], a0[1], a1[0], a1[1]};
+                }
+        };
+        read_weights();
+        read_values();
+        __builtin_amdgcn_sched_barrier(0);
+        if (__builtin_amdgcn_readfirstlane(raise)) {
+            dev::lds_barrier();                          // maxima
+            dev::lds_barrier();                          // weights and factors
+            read_weights();
             const float f0 = sh.fac[l31], f1 = sh.fac[32 + l31];
 #pragma unroll
             for (int cb = 0; cb < 4; ++cb)
@@ -300,60 +348,46 @@ __device__ __forceinline__ void sum_item(const DecodeArgs &a, const DecodeItem &
                     acc[cb][1][i] *= f1;
                 }
         }
-        if (careful && (t + 1) * kStepKeys > sh.open) clean<BF>(sh, t);
-    };
-    const int kr0 = 8 * lh + ((lane >> 2) & 3);
-    auto add_values = [&](int t, bool more) {
-        const uint8_t *vr = sh.ring(t) + 2 * wave * kBlockBytes + 8 * (lane & 1);
-        const uint8_t *pr = sh.weights(t);
-        u32x4 pf[2][2], vf[2][4];
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-#pragma unroll
-            for (int rb = 0; rb < 2; ++rb) pf[k][rb] = *reinterpret_cast<const u32x4 *>(pr + weight_unit(32 * rb + l31, 2 * k + lh));
-#pragma unroll
-            for (int cb = 0; cb < 4; ++cb) {
-                const uint8_t *blk = vr + (cb >> 1) * kBlockBytes + 16 * k * 128;
-                const int unit = 4 * (cb & 1) + 2 * ((lane >> 4) & 1) + ((lane >> 1) & 1);
-                const u32x2 a0 = dev::read_tr(blk + dev::tile_unit(kr0, unit));
-                const u32x2 a1 = dev::read_tr(blk + dev::tile_unit(kr0 + 4, unit));
-                vf[k][cb] = u32x4{a0[0], a0[1], a1[0], a1[1]};
-            }
+        if (careful && (t + 1) * kStepKeys > sh.open) {
+            clean<BF>(sh, t);
+            read_values();
         }
+        Copy next = now;
+        if (more) copy(now, 0);
 #pragma unroll
         for (int k = 0; k < 2; ++k)
 #pragma unroll
-            for (int cb = 0; cb < 4; ++cb)
+            for (int cb = 0; cb < 4; ++cb) {
+                __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
                 for (int rb = 0; rb < 2; ++rb) acc[cb][rb] = dev::mma<BF>(vf[k][cb], pf[k][rb], acc[cb][rb]);
-        __builtin_amdgcn_sched_barrier(0);
-        if (more) copy(0, kBlocks);
+                __builtin_amdgcn_sched_barrier(0);
+                if (more) copy(now, 1 + 4 * k + cb);
+                if (more && k == 1 && cb == 1) {
+                    next = aim(t + 4, page);
+                    page = page_of(t + 5);
+                }
+            }
+        now = next;
     };
 
-    const int pg0 = page_of(sh.t0), pg1 = page_of(sh.t0 + 1);
-    int page = page_of(sh.t0 + 2);
-    aim(sh.t0, pg0);
-    copy(0, kBlocks);
-    aim(sh.t0 + 1, pg1);
-    copy(0, kBlocks);
+    const int pg0 = page_of(sh.t0), pg1 = page_of(sh.t0 + 1), pg2 = page_of(sh.t0 + 2), pg3 = page_of(sh.t0 + 3);
+    int page = page_of(sh.t0 + 4);
+    copy_all(aim(sh.t0, pg0));
+    copy_all(aim(sh.t0 + 1, pg1));
     asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kBlocks) : "memory");
     dev::lds_barrier();                                  // step t0 has landed
-    aim(sh.t0 + 2, page);
-    copy(0, kBlocks);
-    page = page_of(sh.t0 + 3);
+    copy_all(aim(sh.t0 + 2, pg2));
+    Copy now = aim(sh.t0 + 3, pg3);
     dev::lds_barrier();                                  // the first maxima
     for (int t = sh.t0 + 1; t < sh.t1; ++t) {
         // Step t has landed when only the copies of step t + 1 are in flight.
         asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kBlocks) : "memory");
         dev::lds_barrier();
-        aim(t + 2, page);
-        page = page_of(t + 3);
-        settle(t - 1);
-        add_values(t - 1, true);
+        step(t - 1, true, now, page);
     }
     dev::copy_barrier();
-    settle(last);
-    add_values(last, false);
+    step(last, false, now, page);
     float z = 0.0f;
 #pragma unroll
     for (int cb = 0; cb < 4; ++cb)
@@ -364,19 +398,17 @@ __device__ __forceinline__ void sum_item(const DecodeArgs &a, const DecodeItem &
     if (__any(z != 0.0f)) *sh.bad = 1;
 }
 
-// This workgroup's item of the round that starts at item `first`, and its
-// steps; false where it has none.  Neighbouring items share keys: a round's
-// items lie in eight contiguous runs, one per XCD.
-__device__ __forceinline__ bool take_item(const DecodeArgs &a, int first, int n_items, DecodeItem &it, Shared &sh) {
-    const int here = min(static_cast<int>(gridDim.x), n_items - first), run = (here + 7) / 8;
-    const int bx = static_cast<int>(blockIdx.x) & 7, by = static_cast<int>(blockIdx.x) >> 3;
-    if (by >= run || bx * run + by >= here) return false;
+// This workgroup's item of a round (no item: n == 0) and its steps.
+__device__ __forceinline__ DecodeItem take_item(const DecodeArgs &a, int round, bool &more, Shared &sh) {
     typedef int32_t int8v __attribute__((ext_vector_type(8)));
-    it = __builtin_bit_cast(DecodeItem, dev::ld_uniform(reinterpret_cast<const int8v *>(a.plan.items + first + bx * run + by)));
+    DecodeItem it = __builtin_bit_cast(
+        DecodeItem, dev::ld_uniform(reinterpret_cast<const int8v *>(a.plan.items + static_cast<int64_t>(round) * gridDim.x + blockIdx.x)));
+    more = it.seq & kItemMore;
+    it.seq &= ~kItemMore;
     sh.t0 = 2 * it.t0;
     sh.t1 = min(2 * it.t1, (it.len + kStepKeys - 1) / kStepKeys);
     sh.open = it.len - it.n + (a.mask ? 0 : 1);
-    return true;
+    return it;
 }
 
 template <bool BF>
@@ -391,12 +423,12 @@ __global__ __launch_bounds__(kThreads, 2) void latent_decode_kernel(DecodeArgs a
 
     // The two kinds walk the items in loops of their own (and meet at the same
     // barriers): neither then holds registers for the other.
-    const int n_items = dev::ld_uniform(a.plan.head);
+    bool more = true;
     Shared sh{s_kv, s_p, s_red, s_fac, s_sum, s_raise, &s_bad, 0, 0, 0};
     if (wave < 4) {
-        for (int first = 0; first < n_items; first += static_cast<int>(gridDim.x)) {
-            DecodeItem it;
-            if (!take_item(a, first, n_items, it, sh)) continue;
+        for (int round = 0; more; ++round) {
+            const DecodeItem it = take_item(a, round, more, sh);
+            if (it.n == 0) continue;
             const int rows = min(kTileRows, it.n * a.n_heads - it.row0);
             float m[2];
             for (int careful = 0; careful < 2; ++careful) {
@@ -425,9 +457,9 @@ __global__ __launch_bounds__(kThreads, 2) void latent_decode_kernel(DecodeArgs a
     } else {
         const int w = wave - 4;
         bool bad_page = false;
-        for (int first = 0; first < n_items; first += static_cast<int>(gridDim.x)) {
-            DecodeItem it;
-            if (!take_item(a, first, n_items, it, sh)) continue;
+        for (int round = 0; more; ++round) {
+            const DecodeItem it = take_item(a, round, more, sh);
+            if (it.n == 0) continue;
             const int rows = min(kTileRows, it.n * a.n_heads - it.row0);
             f32x16 acc[4][2];                            // [32 columns][32 rows] blocks of O^T
             for (int careful = 0; careful < 2; ++careful) {
@@ -466,29 +498,38 @@ __global__ __launch_bounds__(kThreads, 2) void latent_decode_kernel(DecodeArgs a
 }
 
 // Joins the pieces of a row: with M = max m_i, o = sum 2^(m_i - M) O_i / sum
-// 2^(m_i - M) l_i.  Two rows per 256-thread workgroup, two waves a row, four
-// columns per thread.  Each lane of a wave holds one piece's factor, so the
-// statistics are one load and the partial rows are all in flight together;
-// pieces are summed in a fixed order.
+// 2^(m_i - M) l_i, summed in a fixed order.  Each lane of a wave holds one
+// piece's factor, so the statistics are one load, and eight columns.  Up to
+// kWavePieces pieces a wave joins a row by itself (four rows a workgroup, all
+// partial rows in flight together); more of them are shared by the four
+// waves of a workgroup and added up in LDS.
+constexpr int kWavePieces = 8;
+
 template <bool BF>
 __global__ __launch_bounds__(256) void join_kernel(DecodeArgs a) {
-    const int n = dev::ld_uniform(a.plan.head + 1) * (kTileRows / 2);
-    const int lane = threadIdx.x & 63, half = dev::wave_id() >> 1, col = 4 * (threadIdx.x & 127);
-    for (int w = blockIdx.x; w < n; w += gridDim.x) {
-        const JoinUnit u = a.plan.joins[w / (kTileRows / 2)];
-        const int r = 2 * (w % (kTileRows / 2)) + half;
-        if (r >= u.rows) continue;
+    __shared__ float s_o[4][kLatent];
+    __shared__ float s_l[4];
+    const int joins = dev::ld_uniform(a.plan.head), most = dev::ld_uniform(a.plan.head + 1);
+    const bool apart = most <= kWavePieces;
+    const int per = apart ? kTileRows / 4 : kTileRows;
+    const int lane = threadIdx.x & 63, wave = dev::wave_id();
+    for (int w = blockIdx.x; w < joins * per; w += gridDim.x) {
+        const JoinUnit u = a.plan.joins[w / per];
+        const int r = apart ? 4 * (w % per) + wave : w % per;
+        if (apart ? r >= u.rows : w % per >= u.rows) continue;
         const float *ml = a.part_ml + (static_cast<int64_t>(u.slot0) * kTileRows + r) * 2;
-        const float *part = a.part + (static_cast<int64_t>(u.slot0) * kTileRows + r) * kLatent + col;
+        const float *part = a.part + (static_cast<int64_t>(u.slot0) * kTileRows + r) * kLatent + 4 * lane;
         float top = -__builtin_inff();
         for (int i = lane; i < u.split; i += 64) top = fmaxf(top, ml[i * kTileRows * 2]);
 #pragma unroll
         for (int o = 32; o; o >>= 1) top = fmaxf(top, __shfl_xor(top, o, 64));
         const float ms = top == -__builtin_inff() ? 0.0f : top;
         float l = 0.0f;
-        f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
-        for (int i0 = 0; i0 < u.split; i0 += 64) {
-            const int here = min(64, u.split - i0);
+        f32x4 o[2] = {f32x4{0.0f, 0.0f, 0.0f, 0.0f}, f32x4{0.0f, 0.0f, 0.0f, 0.0f}};
+        // This wave's pieces: all, or a quarter.
+        const int p0 = apart ? 0 : u.split * wave / 4, p1 = apart ? u.split : u.split * (wave + 1) / 4;
+        for (int i0 = p0; i0 < p1; i0 += 64) {
+            const int here = min(64, p1 - i0);
             const float *mine = ml + static_cast<int64_t>(i0 + min(lane, here - 1)) * kTileRows * 2;
             const float f = lane < here ? __builtin_amdgcn_exp2f(mine[0] - ms) : 0.0f;
             float sum = lane < here ? f * mine[1] : 0.0f;
@@ -498,16 +539,36 @@ __global__ __launch_bounds__(256) void join_kernel(DecodeArgs a) {
 #pragma unroll 8
             for (int i = 0; i < here; ++i) {
                 const float fi = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(f), i));
-                const f32x4 v = *reinterpret_cast<const f32x4 *>(part + static_cast<int64_t>(i0 + i) * kTileRows * kLatent);
+                const float *x = part + static_cast<int64_t>(i0 + i) * kTileRows * kLatent;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) o[j] = __builtin_fmaf(fi, v[j], o[j]);
+                for (int h = 0; h < 2; ++h) {
+                    const f32x4 v = *reinterpret_cast<const f32x4 *>(x + 256 * h);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) o[h][j] = __builtin_fmaf(fi, v[j], o[h][j]);
+                }
+            }
+        }
+        if (!apart) {
+            __syncthreads();
+#pragma unroll
+            for (int h = 0; h < 2; ++h) *reinterpret_cast<f32x4 *>(&s_o[wave][4 * lane + 256 * h]) = o[h];
+            if (lane == 0) s_l[wave] = l;
+            __syncthreads();
+            if (wave != 0) continue;
+#pragma unroll
+            for (int k = 1; k < 4; ++k) {
+                l += s_l[k];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) o[h] += *reinterpret_cast<const f32x4 *>(&s_o[k][4 * lane + 256 * h]);
             }
         }
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
         const int64_t row = u.out_row + r;
-        *reinterpret_cast<u32x2 *>(a.out + (row * kLatent + col) * 2) =
-            u32x2{dev::pack2<BF>(o[0] * inv, o[1] * inv), dev::pack2<BF>(o[2] * inv, o[3] * inv)};
-        if (a.lse && col == 0) a.lse[row] = l == 0.0f ? -__builtin_inff() : (top + __builtin_amdgcn_logf(l)) * kLn2;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            *reinterpret_cast<u32x2 *>(a.out + (row * kLatent + 4 * lane + 256 * h) * 2) =
+                u32x2{dev::pack2<BF>(o[h][0] * inv, o[h][1] * inv), dev::pack2<BF>(o[h][2] * inv, o[h][3] * inv)};
+        if (a.lse && lane == 0) a.lse[row] = l == 0.0f ? -__builtin_inff() : (top + __builtin_amdgcn_logf(l)) * kLn2;
     }
 }
 
@@ -594,6 +655,7 @@ __global__ __launch_bounds__(kPlanThreads) void decode_plan_kernel(DecodePlan p,
     if (best < 1) best = 1;
 
     int n_items = 0, n_slots = 0, n_joins = 0;
+    if (tid == 0) s_most = 1;
     for (int b0 = 0; b0 < n_seq; b0 += kPlanThreads) {
         const int b = b0 + tid;
         int4 s = b < n_seq ? seq[b] : int4{0, 0, 0, 0};
@@ -609,15 +671,33 @@ __global__ __launch_bounds__(kPlanThreads) void decode_plan_kernel(DecodePlan p,
             s.z = at;
             s.w = split > 1 ? slot : -1;
             seq[b] = s;
-            if (split > 1 && slot + count <= p.slot_cap) {
+            if (split > 1 && s.x) atomicMax(&s_most, split);
+            if (split > 1 && slot + count <= p.slot_cap && join + s.x <= p.join_cap) {
                 const int q0 = q_start[b], rows = (q_start[b + 1] - q0) * n_heads;
                 for (int i = 0; i < s.x; ++i)
                     p.joins[join + i] = JoinUnit{q0 * n_heads + i * kTileRows, min(kTileRows, rows - i * kTileRows), slot + i * split, split};
             }
         }
     }
-    const bool fits = n_items <= p.item_cap && n_slots <= p.slot_cap;
+    // Round r, place x: workgroup x runs on XCD x % 8, and neighbouring items
+    // share keys, so a round's items lie in eight contiguous runs, one per XCD.
+    const int rounds = max(1, (n_items + n_cu - 1) / n_cu);
+    const bool fits = rounds * n_cu <= p.item_cap && n_slots <= p.slot_cap && n_joins <= p.join_cap;
+    auto place = [&](int i) {
+        const int r = i / n_cu, at = i - r * n_cu, here = min(n_cu, n_items - r * n_cu), run = (here + 7) / 8;
+        return r * n_cu + (at % run) * 8 + at / run;
+    };
     __syncthreads();
+    {
+        for (int i = tid; i < (fits ? rounds : 1) * n_cu; i += kPlanThreads) {
+            const int r = i / n_cu, x = i - r * n_cu, here = fits ? min(n_cu, n_items - r * n_cu) : 0, run = (here + 7) / 8;
+            if ((x >> 3) >= run || (x & 7) * run + (x >> 3) >= here) {
+                DecodeItem none{};
+                none.seq = r + 1 < rounds && fits ? kItemMore : 0;
+                p.items[i] = none;
+            }
+        }
+    }
     if (fits)
         for (int b = wave; b < n_seq; b += kPlanThreads / 64) {
             const int4 s = seq[b];
@@ -629,17 +709,17 @@ __global__ __launch_bounds__(kPlanThreads) void decode_plan_kernel(DecodePlan p,
                 it.q0 = q0;
                 it.n = n;
                 it.len = len;
-                it.seq = b;
+                it.seq = b | ((s.z + i) / n_cu + 1 < rounds ? kItemMore : 0);
                 it.row0 = u * kTileRows;
                 it.t0 = static_cast<int>(static_cast<int64_t>(s.y) * c / split);
                 it.t1 = static_cast<int>(static_cast<int64_t>(s.y) * (c + 1) / split);
                 it.slot = s.w < 0 ? -1 : s.w + u * split + c;
-                p.items[s.z + i] = it;
+                p.items[place(s.z + i)] = it;
             }
         }
     if (tid == 0) {
-        p.head[0] = fits ? n_items : 0;
-        p.head[1] = fits ? n_joins : 0;
+        p.head[0] = fits ? n_joins : 0;
+        p.head[1] = s_most;
     }
     dev::flag_if(bad || !fits, err, kErrSeq);
 }
@@ -657,7 +737,8 @@ hipError_t launch_latent_decode(const DecodeArgs &a, bool bf16, int n_cu, hipStr
     launch(bf16 ? latent_decode_kernel<true> : latent_decode_kernel<false>, static_cast<unsigned>(n_cu), kThreads, 0, s, a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    launch(bf16 ? join_kernel<true> : join_kernel<false>, static_cast<unsigned>(2 * n_cu), 256u, 0, s, a);
+    const unsigned blocks = static_cast<unsigned>(std::min<int64_t>(static_cast<int64_t>(a.join_most) * kTileRows, 8 * n_cu));
+    launch(bf16 ? join_kernel<true> : join_kernel<false>, blocks, 256u, 0, s, a);
     return hipGetLastError();
 }
 

@@ -22,22 +22,24 @@ constexpr int32_t kErrNoMass = 8;     // no token of a row has a positive probab
 
 // One piece of absorbed attention: 64 rows of one sequence against the key
 // tiles [t0, t1).  slot >= 0: a partial result, joined with the other pieces
-// of its rows afterwards.
+// of its rows afterwards.  Items are laid out in rounds of one per workgroup;
+// n == 0 is a place without one.
 struct alignas(32) DecodeItem {
-    int32_t q0, n, len, seq;   // first token, tokens and cached length of the sequence
+    int32_t q0, n, len, seq;   // first token, tokens and cached length of the sequence; seq | kItemMore: rounds follow
     int32_t row0, t0, t1, slot;
 };
+constexpr int32_t kItemMore = 1 << 30;
 // Rows whose pieces are joined: `rows` output rows from out_row, the partials
 // slot0 .. slot0 + split - 1.
 struct alignas(16) JoinUnit {
     int32_t out_row, rows, slot0, split;
 };
 struct DecodePlan {
-    int32_t *head;             // [2] items, join units
+    int32_t *head;             // [2] join units, the most pieces of one
     DecodeItem *items;
     JoinUnit *joins;
     int32_t *seq;              // [max_seqs x 4] scratch of the planning
-    int item_cap, slot_cap;
+    int item_cap, join_cap, slot_cap;
 };
 
 struct CacheView {
@@ -60,6 +62,7 @@ struct DecodeArgs {
     uint8_t *out;              // [n_tok x n_heads x 512]
     float *lse;                // [n_tok x n_heads] or NULL
     DecodePlan plan;
+    int join_most;             // at least the plan's join units
     float *part;               // [slot_cap x 64 x 512]
     float *part_ml;            // [slot_cap x 64 x 2]
     int32_t *err;

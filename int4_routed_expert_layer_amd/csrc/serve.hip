@@ -2,6 +2,7 @@
 // include/coli_moe.h: the handle with its plan and scratch, argument checks,
 // launches.
 #include <cstdarg>
+#include <algorithm>
 #include <cmath>
 #include <cstdio>
 #include <new>
@@ -73,7 +74,8 @@ struct Sizes {
 Sizes plan_sizes(const coli_serve_dims &d, int n_cu) {
     const int64_t units = static_cast<int64_t>(d.max_tokens) * d.n_heads / kTileRows + d.max_seqs;
     const int64_t slots = 4ll * n_cu;
-    return Sizes{units + slots, units, slots, d.max_seqs};
+    const int64_t rounds = (units + slots + n_cu - 1) / n_cu + 1;
+    return Sizes{rounds * n_cu, std::min(units, slots / 2), slots, d.max_seqs};
 }
 size_t create_bytes(const coli_serve_dims &d, int n_cu) {
     const Sizes z = plan_sizes(d, n_cu);
@@ -161,9 +163,11 @@ coli_status coli_serve_create(const coli_serve_dims *d, int device, coli_serve *
     if (!S) return fail(nullptr, COLI_E_NOMEM, "no host memory for the handle");
     S->d = *d;
     S->device = device;
-    S->n_cu = n_cu;
+    S->n_cu = std::max(8, n_cu / 8 * 8);   // workgroups of a round: the same number on each of eight XCDs
+    n_cu = S->n_cu;
     const Sizes z = plan_sizes(*d, n_cu);
     S->plan.item_cap = static_cast<int>(z.items);
+    S->plan.join_cap = static_cast<int>(z.joins);
     S->plan.slot_cap = static_cast<int>(z.slots);
     struct { void **p; size_t n; const char *what; } allocs[] = {
         {reinterpret_cast<void **>(&S->plan.head), 2 * sizeof(int32_t), "plan head"},
@@ -187,6 +191,7 @@ coli_status coli_serve_create(const coli_serve_dims *d, int device, coli_serve *
     if ((he = hipMemset(S->best, 0, z.seqs * 2 * sizeof(uint64_t))) != hipSuccess ||
         (he = hipMemset(S->arrived, 0, z.seqs * sizeof(int32_t))) != hipSuccess ||
         (he = hipMemset(S->plan.head, 0, 2 * sizeof(int32_t))) != hipSuccess ||
+        (he = hipMemset(S->plan.items, 0, z.items * sizeof(DecodeItem))) != hipSuccess ||
         (he = hipMemset(S->err, 0, sizeof(int32_t))) != hipSuccess || (he = hipDeviceSynchronize()) != hipSuccess) {
         fail(nullptr, COLI_E_DEVICE, "handle setup: %s", hipGetErrorString(he));
         free_serve(S);
@@ -327,6 +332,8 @@ coli_status coli_latent_decode(coli_serve *S, const void *q_lat, int64_t ql_tok_
     a.out = static_cast<uint8_t *>(out);
     a.lse = lse;
     a.plan = S->plan;
+    // A joined unit has two pieces at least.
+    a.join_most = static_cast<int>(std::min<int64_t>(S->plan.join_cap, static_cast<int64_t>(n_tok) * S->d.n_heads / kTileRows + S->plan_seq));
     a.part = S->part;
     a.part_ml = S->part_ml;
     a.err = S->err;
