@@ -7,13 +7,13 @@
 // rotary part from its own rows, so no key is ever assembled in memory.
 //
 // A 512-thread workgroup (two waves per SIMD) takes 256 query rows of one head,
-// 32 per wave, and walks 64-key tiles that are copied straight into LDS,
-// double buffered.  S^T = K Q^T leaves lane L with row L % 32 of its wave and
-// half of the keys; rounded to 16 bits those registers are the second
+// 32 per wave, and walks the keys in steps of 32 that are copied straight into
+// LDS, a ring of four.  S^T = K Q^T leaves lane L with row L % 32 of its wave
+// and half of the keys; rounded to 16 bits those registers are the second
 // product's B operand as they stand, because the order of keys inside a K step
 // is free as long as V^T (transposed LDS reads) takes them in the same order.
 // Softmax statistics never leave the wave, and the only barrier is the one
-// that turns the buffers.
+// that turns the ring.
 #include "dev_attn.h"
 
 namespace coli {
@@ -23,42 +23,228 @@ using dev::f32x16;
 using dev::u32x2;
 using dev::u32x4;
 
-constexpr int kBlockBytes = kTileKeys * 128;
+constexpr int kStepKeys = 32;
+constexpr int kBlockBytes = kStepKeys * 128;
+constexpr int kRing = 4;
 constexpr float kSlack = 8.0f;    // see latent_decode.hip
 constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.69314718055994531f;
 constexpr int kWaves = 8;
 constexpr int kRows = 32 * kWaves;
+constexpr int kAhead = 4;         // LDS reads in flight ahead of the products that use them
 
-template <bool BF, int NOPE, int V>
-__global__ __launch_bounds__(64 * kWaves, 2) void latent_prompt_kernel(PromptArgs a, int tiles_cap) {
-    constexpr int kKeyBlocks = (NOPE + kRope) / 64, kNopeBlocks = NOPE / 64, kValueBlocks = V / 64;
-    constexpr int kSteps = (NOPE + kRope) / 16, kBlocks = kKeyBlocks + kValueBlocks;
-    constexpr int kTileBytes = kBlocks * kBlockBytes;
-    __shared__ __align__(1024) uint8_t s_kv[2 * kTileBytes];
-    __shared__ int s_bad;
-    const int tid = threadIdx.x, lane = tid & 63, wave = dev::wave_id();
-    const int l31 = lane & 31, lh = lane >> 5;
-    const uint32_t kv_lds = dev::lds_address(s_kv);
+// The widths of one head, in 64-column blocks of the LDS step.
+template <int NOPE, int V>
+struct Head {
+    static constexpr int kKeyBlocks = (NOPE + kRope) / 64, kNopeBlocks = NOPE / 64, kValueBlocks = V / 64;
+    static constexpr int kDepth = (NOPE + kRope) / 16;          // K steps of the first product
+    static constexpr int kBlocks = kKeyBlocks + kValueBlocks;
+    static constexpr int kStepBytes = kBlocks * kBlockBytes;
+};
+
+// One row tile of one head.
+struct Tile {
+    int q0, k0, nk;            // first query token and key of the sequence, its keys
+    int head, row0, rows;      // rows row0 .. row0 + rows - 1 of the sequence's queries
+    int ahead;                 // row i sees keys up to i + ahead (causal)
+    int steps;
+};
+
+// The keys a row of the tile sees (the first `seen` ones).
+__device__ __forceinline__ int seen_by(const PromptArgs &a, const Tile &t, int row) {
+    return a.causal ? min(t.nk, t.row0 + row + t.ahead + 1) : t.nk;
+}
+
+// Attention of the wave's 32 rows over all steps.  CAREFUL: keys that a row does
+// not see have weight zero, and zero times inf or NaN must not reach it; values
+// that are not finite are taken as zero where a step hides keys, and a second
+// product counts, per output, those that the row does see, which make that
+// output NaN.
+template <bool BF, int NOPE, int V, bool CAREFUL>
+__device__ __forceinline__ void attend(const PromptArgs &a, const Tile &tile, uint8_t *s_kv, uint32_t kv_lds, f32x16 (&acc)[V / 32],
+                                       float &m, float &l) {
+    using H = Head<NOPE, V>;
+    const int lane = threadIdx.x & 63, wave = dev::wave_id(), l31 = lane & 31, lh = lane >> 5;
     const float c = a.scale * kLog2e;
+    const int row = 32 * wave + l31;
+    // Keys below `open` are seen by every row of the wave, from `shut` on by none.
+    const int open = seen_by(a, tile, 32 * wave), shut = seen_by(a, tile, min(32 * wave + 31, tile.rows - 1));
+    const int seen_all = seen_by(a, tile, row);
 
-    // Workgroups of one XCD (blockIdx % 8) take the row tiles of the same
-    // heads, which share K and V in its L2; the last tiles, which see the most
-    // keys, come first.
+    u32x4 q[H::kDepth];
+    {
+        const int qrow = tile.q0 + tile.row0 + min(row, tile.rows - 1);
+        const uint8_t *src = a.q + (static_cast<int64_t>(qrow) * a.q_tok + tile.head * a.q_head) * 2 + 16 * lh;
+#pragma unroll
+        for (int k = 0; k < H::kDepth; ++k) q[k] = dev::gload<u32x4>(src + 32 * k);
+    }
+
+    // Copies.  A step is kBlocks x 32 rows x 128 bytes: piece i of it is rows
+    // 8 (i % 4) .. + 7 of block i / 4, one copy of a wave; wave w takes
+    // those rows w % 4 of every other block.
+    constexpr int kPieces = H::kBlocks * 4, kMine = (kPieces + kWaves - 1) / kWaves;
+    auto copy_step = [&](int t) {
+        t = min(t, tile.steps - 1);                       // past the end the last step is copied again
+        const int cr = 8 * (wave & 3) + (lane >> 3);
+        const int64_t key = tile.k0 + min(t * kStepKeys + cr, tile.nk - 1);
+        const int unit = ((lane & 7) ^ dev::tile_swz(cr)) << 4;
+        const uint8_t *kv = a.kv + (key * a.kv_tok + tile.head * a.kv_head) * 2 + unit;
+        const uint8_t *pe = a.k_pe + key * a.pe_tok * 2 + unit;
+        const uint32_t dst = kv_lds + (t & (kRing - 1)) * H::kStepBytes + (wave & 3) * 1024;
+#pragma unroll
+        for (int i = 0; i < kMine; ++i) {
+            const int b = 2 * i + (wave >> 2);            // blocks 0, 2, .. or 1, 3, ..
+            if (H::kBlocks % 2 && i == kMine - 1 && b >= H::kBlocks) break;
+            const uint8_t *src = b < H::kNopeBlocks ? kv + b * 128 : b == H::kNopeBlocks ? pe : kv + (b - 1) * 128;
+            dev::copy16_to_lds(src, dst + b * kBlockBytes);
+        }
+    };
+    // Copies of a wave per step, the same for every step.
+    const int each = H::kBlocks % 2 ? kMine - (wave >> 2) : kMine;
+
+#pragma unroll
+    for (int cb = 0; cb < V / 32; ++cb)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) acc[cb][i] = 0.0f;
+    m = -__builtin_inff();
+    l = 0.0f;
+    float limit = -__builtin_inff(), offset = 0.0f;       // of a score that calls for a new maximum; of the exponent
+    if (tile.steps == 0) return;
+    copy_step(0);
+    copy_step(1);
+    for (int t = 0; t < tile.steps; ++t) {
+        // Step t has landed when only the copies of step t + 1 are in flight.
+        if (H::kBlocks % 2 == 0 || each == kMine)
+            asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kMine) : "memory");
+        else
+            asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kMine - 1) : "memory");
+        dev::lds_barrier();
+        copy_step(t + 2);
+        if (t * kStepKeys >= shut) continue;
+        const uint8_t *kv = s_kv + (t & (kRing - 1)) * H::kStepBytes;
+        auto key = [&](int k) { return *reinterpret_cast<const u32x4 *>(kv + (k >> 2) * kBlockBytes + dev::tile_unit(l31, 2 * (k & 3) + lh)); };
+        f32x16 s;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s[i] = 0.0f;
+        u32x4 kf[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) kf[k] = key(k);
+#pragma unroll
+        for (int k = 0; k < H::kDepth; ++k) {
+            s = dev::mma<BF>(kf[k % kAhead], q[k], s);
+            if (k + kAhead < H::kDepth) kf[k % kAhead] = key(k + kAhead);
+        }
+        dev::pipeline<H::kDepth, 1, 1, kAhead>();
+        __builtin_amdgcn_sched_barrier(0);
+        const bool masked = (t + 1) * kStepKeys > open;
+        const int seen = seen_all - t * kStepKeys - 4 * lh;
+        if (masked) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                if (8 * (i >> 2) + (i & 3) >= seen) s[i] = -__builtin_inff();
+        }
+        float mx = s[0];
+#pragma unroll
+        for (int i = 1; i < 16; ++i) mx = fmaxf(mx, s[i]);
+        if (__any(mx > limit)) {
+            // The maximum of a row moves only when a step exceeds it by more
+            // than the slack.
+            const float tm = dev::max_halves(mx) * c;
+            const float m1 = tm > m + (m == -__builtin_inff() ? 0.0f : kSlack) ? tm : m;
+            const float fac = m1 == m ? 1.0f : __builtin_amdgcn_exp2f(m - m1);
+            m = m1;
+            l *= fac;
+            limit = m == -__builtin_inff() ? m : (m + kSlack) / c;
+            offset = m == -__builtin_inff() ? 0.0f : -m;
+#pragma unroll
+            for (int cb = 0; cb < V / 32; ++cb)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) acc[cb][i] *= fac;
+        }
+        u32x4 p[2];                                       // B operands of the two 16-key products
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float e0 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[2 * j], c, offset));
+            const float e1 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[2 * j + 1], c, offset));
+            l += e0 + e1;
+            p[j >> 2][j & 3] = dev::pack2<BF>(e0, e1);
+        }
+        // O^T: product k takes keys 16 k + 4 lh + 0..3 and 16 k + 8 + 4 lh + 0..3.
+        const uint8_t *vt = kv + H::kKeyBlocks * kBlockBytes + 8 * (lane & 1);
+        const int vr = 4 * lh + ((lane >> 2) & 3);
+        auto value = [&](int n) {                         // of product n: 16 keys n / (V / 32), columns 32 (n % (V / 32))
+            const int k = n / (V / 32), cb = n % (V / 32);
+            const uint8_t *blk = vt + (cb >> 1) * kBlockBytes + 16 * k * 128;
+            const int unit = 4 * (cb & 1) + 2 * ((lane >> 4) & 1) + ((lane >> 1) & 1);
+            const u32x2 a0 = dev::read_tr(blk + dev::tile_unit(vr, unit));
+            const u32x2 a1 = dev::read_tr(blk + dev::tile_unit(vr + 8, unit));
+            return u32x4{a0[0], a0[1], a1[0], a1[1]};
+        };
+        if (CAREFUL && masked) {
+            const uint32_t one = BF ? 0x3F80u : 0x3C00u;
+#pragma unroll
+            for (int cb = 0; cb < V / 32; ++cb) {
+                f32x16 n;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) n[i] = 0.0f;
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    u32x4 v = value(k * (V / 32) + cb), off, sees;
+#pragma unroll
+                    for (int d = 0; d < 4; ++d) {
+                        const uint32_t x = dev::nonfinite_halves<BF>(v[d]);
+                        v[d] &= ~x;
+                        off[d] = x & (one | one << 16);
+                        const int at = 16 * k + 8 * (d >> 1) + 2 * (d & 1);
+                        sees[d] = (at < seen ? one : 0u) | (at + 1 < seen ? one << 16 : 0u);
+                    }
+                    acc[cb] = dev::mma<BF>(v, p[k], acc[cb]);
+                    n = dev::mma<BF>(off, sees, n);
+                }
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (n[i] > 0.0f) acc[cb][i] = __builtin_nanf("");
+            }
+        } else {
+            __builtin_amdgcn_sched_barrier(0);
+            constexpr int kN = 2 * (V / 32);
+            u32x4 vf[kAhead];
+#pragma unroll
+            for (int n = 0; n < kAhead; ++n) vf[n] = value(n);
+#pragma unroll
+            for (int n = 0; n < kN; ++n) {
+                acc[n % (V / 32)] = dev::mma<BF>(vf[n % kAhead], p[n / (V / 32)], acc[n % (V / 32)]);
+                if (n + kAhead < kN) vf[n % kAhead] = value(n + kAhead);
+            }
+            dev::pipeline<2 * kN, 1, 2, 2 * kAhead>();
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    }
+    // The copies past the end land before the ring is used again.
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+}
+
+// The row tile (of ROWS rows) of this workgroup; false where it has none.
+// Workgroups of one XCD (blockIdx % 8) take the row tiles of the same heads,
+// which share K and V in its L2; the last tiles, which see the most keys,
+// come first.
+template <int ROWS>
+__device__ __forceinline__ bool find_tile(const PromptArgs &a, int tiles_cap, Tile &tile) {
+    const int lane = threadIdx.x & 63;
     const int total = a.n_heads * tiles_cap, share = (total + 7) / 8;
     const int lin = static_cast<int>(blockIdx.x & 7) * share + static_cast<int>(blockIdx.x >> 3);
-    if (static_cast<int>(blockIdx.x >> 3) >= share || lin >= total) return;
-    const int head = lin / tiles_cap, want = tiles_cap - 1 - (lin - head * tiles_cap);
-
+    if (static_cast<int>(blockIdx.x >> 3) >= share || lin >= total) return false;
+    tile.head = lin / tiles_cap;
+    const int want = tiles_cap - 1 - (lin - tile.head * tiles_cap);
     // Sequence and row tile number `want` of the call: each lane counts one
     // sequence's tiles.
-    int seq = -1, tile = 0;
+    int seq = -1, number = 0;
     bool bad_seq = false;
     for (int b0 = 0, done = 0; b0 < a.n_seq; b0 += 64) {
         const int b = b0 + lane;
         int n = 0;
         if (b < a.n_seq) {
             const int q0 = a.q_start[b], q1 = a.q_start[b + 1];
-            if (q0 >= 0 && q1 >= q0 && q1 <= a.n_q) n = (q1 - q0 + kRows - 1) / kRows;
+            if (q0 >= 0 && q1 >= q0 && q1 <= a.n_q) n = (q1 - q0 + ROWS - 1) / ROWS;
             else bad_seq = true;
         }
         int cum = n;
@@ -71,207 +257,382 @@ __global__ __launch_bounds__(64 * kWaves, 2) void latent_prompt_kernel(PromptArg
         if (hit) {
             const int at = __ffsll(static_cast<unsigned long long>(hit)) - 1;
             seq = b0 + at;
-            tile = want - done - (__shfl(cum, at, 64) - __shfl(n, at, 64));
+            number = want - done - (__shfl(cum, at, 64) - __shfl(n, at, 64));
             break;
         }
         done += __shfl(cum, 63, 64);
     }
     dev::flag_if(bad_seq, a.err, kErrSeq);
     seq = __builtin_amdgcn_readfirstlane(seq);
-    tile = __builtin_amdgcn_readfirstlane(tile);
-    if (seq < 0) return;
-    const int q0 = a.q_start[seq], nq = a.q_start[seq + 1] - q0;
-    int k0 = a.k_start[seq], nk = a.k_start[seq + 1] - k0;
-    if (k0 < 0 || nk < 0 || nk > a.n_k - k0) {
-        dev::flag_if(tid == 0, a.err, kErrSeq);
-        k0 = nk = 0;
+    number = __builtin_amdgcn_readfirstlane(number);
+    if (seq < 0) return false;
+    tile.q0 = dev::ld_uniform(a.q_start + seq);
+    const int nq = dev::ld_uniform(a.q_start + seq + 1) - tile.q0;
+    tile.k0 = dev::ld_uniform(a.k_start + seq);
+    tile.nk = dev::ld_uniform(a.k_start + seq + 1) - tile.k0;
+    if (tile.k0 < 0 || tile.nk < 0 || tile.nk > a.n_k - tile.k0) {
+        dev::flag_if(threadIdx.x == 0, a.err, kErrSeq);
+        tile.k0 = tile.nk = 0;
     }
-    const int row0 = tile * kRows, rows = min(kRows, nq - row0);
-    const int row = 32 * wave + l31, qrow = row0 + min(row, rows - 1);
-    const int ahead = nk - nq;                            // row i sees keys up to i + ahead
-    const int last = a.causal ? min(nk, row0 + rows + ahead) : nk;
-    const int n_tiles = last > 0 ? (last + kTileKeys - 1) / kTileKeys : 0;
-    // Keys below `open` are seen by every row of the wave; keys from `shut` on
-    // by none.
-    const int open = a.causal ? min(nk, row0 + 32 * wave + ahead + 1) : nk;
-    const int shut = a.causal ? min(nk, row0 + min(32 * wave + 32, rows) + ahead) : nk;
+    tile.row0 = number * ROWS;
+    tile.rows = min(ROWS, nq - tile.row0);
+    tile.ahead = tile.nk - nq;
+    const int last = seen_by(a, tile, tile.rows - 1);
+    tile.steps = last > 0 ? (last + kStepKeys - 1) / kStepKeys : 0;
+    return true;
+}
 
-    u32x4 q[kSteps];
-    {
-        const uint8_t *src = a.q + (static_cast<int64_t>(q0 + qrow) * a.q_tok + head * a.q_head) * 2 + 16 * lh;
-#pragma unroll
-        for (int k = 0; k < kSteps; ++k) q[k] = dev::gload<u32x4>(src + 32 * k);
-    }
-
-    // Copies: each wave fetches eight keys, a 16-byte unit per lane and block.
-    const int cr = 8 * wave + (lane >> 3);
-    const int cu = ((lane & 7) ^ dev::tile_swz(cr)) << 4;
-    auto copy_tile = [&](int t, int buf) {
-        const int64_t key = k0 + min(t * kTileKeys + cr, nk - 1);
-        const uint8_t *src = a.kv + (key * a.kv_tok + head * a.kv_head) * 2 + cu;
-        const uint8_t *pe = a.k_pe + key * a.pe_tok * 2 + cu;
-        const uint32_t dst = kv_lds + buf * kTileBytes + wave * 1024;
-#pragma unroll
-        for (int b = 0; b < kNopeBlocks; ++b) dev::copy16_to_lds(src + b * 128, dst + b * kBlockBytes);
-        dev::copy16_to_lds(pe, dst + kNopeBlocks * kBlockBytes);
-#pragma unroll
-        for (int b = 0; b < kValueBlocks; ++b)
-            dev::copy16_to_lds(src + (kNopeBlocks + b) * 128, dst + (kKeyBlocks + b) * kBlockBytes);
-    };
+template <bool BF, int NOPE, int V>
+__global__ __launch_bounds__(64 * kWaves, 2) void latent_prompt_kernel(PromptArgs a, int tiles_cap) {
+    __shared__ __align__(1024) uint8_t s_kv[kRing * Head<NOPE, V>::kStepBytes];
+    __shared__ int s_bad;
+    const int tid = threadIdx.x, lane = tid & 63, wave = dev::wave_id();
+    const int l31 = lane & 31, lh = lane >> 5;
+    const uint32_t kv_lds = dev::lds_address(s_kv);
+    Tile tile;
+    if (!find_tile<kRows>(a, tiles_cap, tile)) return;
 
     f32x16 acc[V / 32];                                   // [32 columns][32 rows] blocks of O^T
     float m, l;
-    for (int careful = 0; careful < 2; ++careful) {
+    if (tid == 0) s_bad = 0;
+    attend<BF, NOPE, V, false>(a, tile, s_kv, kv_lds, acc, m, l);
+    // Anything that is not finite: again with care, if a step hides keys.
+    float z = 0.0f;
 #pragma unroll
-        for (int cb = 0; cb < V / 32; ++cb)
+    for (int cb = 0; cb < V / 32; ++cb)
 #pragma unroll
-            for (int i = 0; i < 16; ++i) acc[cb][i] = 0.0f;
-        m = -__builtin_inff();
-        l = 0.0f;
-        dev::lds_barrier();                               // the buffers of the pass before are free
-        if (tid == 0) s_bad = 0;
-        if (n_tiles) copy_tile(0, 0);
-        for (int t = 0; t < n_tiles; ++t) {
-            const int buf = t & 1;
-            const uint8_t *kv = s_kv + buf * kTileBytes;
-            dev::copy_barrier();
-            if (t + 1 < n_tiles) copy_tile(t + 1, buf ^ 1);
-            if (t * kTileKeys >= shut) continue;
-            f32x16 s[2];
+        for (int i = 0; i < 16; ++i) z = __builtin_fmaf(acc[cb][i], 0.0f, z);
+    dev::lds_barrier();
+    if (__any(z != 0.0f)) s_bad = 1;
+    dev::lds_barrier();
+    if (s_bad) attend<BF, NOPE, V, true>(a, tile, s_kv, kv_lds, acc, m, l);
+
+    const int row = 32 * wave + l31;
+    l = dev::sum_halves(l);
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    const int64_t out_row = static_cast<int64_t>(tile.q0 + tile.row0 + row) * a.n_heads + tile.head;
+    uint8_t *o = row < tile.rows ? a.out + out_row * V * 2 : nullptr;
 #pragma unroll
-            for (int kb = 0; kb < 2; ++kb)
+    for (int cb = 0; cb < V / 32; ++cb) dev::store_tile16<BF>(acc[cb], inv, o ? o + 64 * cb : nullptr);
+    if (a.lse && lh == 0 && row < tile.rows)
+        a.lse[out_row] = l == 0.0f ? -__builtin_inff() : (m + __builtin_amdgcn_logf(l)) * kLn2;
+}
+
+// ---- The wide head: scoring and summing waves ------------------------------
+//
+// A wave with 32 rows of queries (64 registers) and of outputs (128) leaves too
+// little of its 256 registers to the fragments in flight.  The wide head
+// therefore divides the work by kind, as latent_decode.hip does: 128 rows a
+// workgroup; four scoring waves with 32 rows each write the 16-bit
+// probabilities of step t to LDS, four summing waves with a quarter of the
+// value columns each add step t - 1 for all rows and copy step t + 2.  Each
+// SIMD holds one of either kind.  A row's scores lie in one wave, which moves
+// its maximum by itself and leaves the rows' factors for the summing waves.
+constexpr int kSplitRows = 128;
+constexpr int kSplitThreads = 512;
+
+__device__ __forceinline__ int weight_unit(int r, int q) { return r * 64 + ((q ^ ((r >> 2) & 3)) << 4); }
+
+struct Shared {
+    uint8_t *kv, *p;           // [kRing] steps of keys and values; [2] steps of probabilities
+    float *fac, *sum;          // [2][128] factors by step parity; [128] row sums
+    int *raise;                // [3][4] by step and scoring wave: factors to apply
+};
+
+template <bool BF, int NOPE, int V>
+__device__ __forceinline__ void score_rows(const PromptArgs &a, const Tile &tile, const Shared &sh, float &m) {
+    using H = Head<NOPE, V>;
+    const int lane = threadIdx.x & 63, wave = dev::wave_id(), l31 = lane & 31, lh = lane >> 5;
+    const float c = a.scale * kLog2e;
+    const int row = 32 * wave + l31;
+    // Keys below `open` are seen by every row of the wave, from `shut` on by none.
+    const int open = seen_by(a, tile, 32 * wave);
+    const int shut = 32 * wave < tile.rows ? seen_by(a, tile, min(32 * wave + 31, tile.rows - 1)) : 0;
+    const int seen_all = seen_by(a, tile, row);
+    u32x4 q[H::kDepth];
+    {
+        const int qrow = tile.q0 + tile.row0 + min(row, tile.rows - 1);
+        const uint8_t *src = a.q + (static_cast<int64_t>(qrow) * a.q_tok + tile.head * a.q_head) * 2 + 16 * lh;
 #pragma unroll
-                for (int i = 0; i < 16; ++i) s[kb][i] = 0.0f;
+        for (int k = 0; k < H::kDepth; ++k) q[k] = dev::gload<u32x4>(src + 32 * k);
+    }
+    __builtin_amdgcn_s_setprio(2);   // the step waits for these waves: the summing ones fill what they leave
+    m = -__builtin_inff();
+    float l = 0.0f, limit = -__builtin_inff(), offset = 0.0f;
+    for (int t = 0; t < tile.steps; ++t) {
+        dev::lds_barrier();
+        if (lane == 0) sh.raise[((t + 1) % 3) * 4 + wave] = 0;
+        uint8_t *pw = sh.p + (t & 1) * (kSplitRows * 64);
+        if (t * kStepKeys >= shut) {
 #pragma unroll
-            for (int k = 0; k < kSteps; ++k) {
-                const uint8_t *blk = kv + (k >> 2) * kBlockBytes;
+            for (int g = 0; g < 4; ++g) *reinterpret_cast<u32x2 *>(pw + weight_unit(row, g) + 8 * lh) = u32x2{0, 0};
+            continue;
+        }
+        const uint8_t *kv = sh.kv + (t & (kRing - 1)) * H::kStepBytes;
+        auto key = [&](int k) { return *reinterpret_cast<const u32x4 *>(kv + (k >> 2) * kBlockBytes + dev::tile_unit(l31, 2 * (k & 3) + lh)); };
+        f32x16 s[2];
 #pragma unroll
-                for (int kb = 0; kb < 2; ++kb) {
-                    const u32x4 kf = *reinterpret_cast<const u32x4 *>(blk + kb * 32 * 128 + dev::tile_unit(l31, 2 * (k & 3) + lh));
-                    s[kb] = dev::mma<BF>(kf, q[k], s[kb]);
-                }
+        for (int i = 0; i < 16; ++i) s[0][i] = s[1][i] = 0.0f;
+        u32x4 kf[6];
+#pragma unroll
+        for (int k = 0; k < 6; ++k) kf[k] = key(k);
+#pragma unroll
+        for (int k = 0; k < H::kDepth; ++k) {
+            s[k & 1] = dev::mma<BF>(kf[k % 6], q[k], s[k & 1]);
+            if (k + 6 < H::kDepth) kf[k % 6] = key(k + 6);
+        }
+        dev::pipeline<H::kDepth, 1, 1, 6>();
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s[0][i] += s[1][i];
+        if ((t + 1) * kStepKeys > open) {
+            const int seen = seen_all - t * kStepKeys - 4 * lh;
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                if (8 * (i >> 2) + (i & 3) >= seen) s[0][i] = -__builtin_inff();
+        }
+        float mx = s[0][0];
+#pragma unroll
+        for (int i = 1; i < 16; ++i) mx = fmaxf(mx, s[0][i]);
+        if (__any(mx > limit)) {
+            const float tm = dev::max_halves(mx) * c;
+            const float m1 = tm > m + (m == -__builtin_inff() ? 0.0f : kSlack) ? tm : m;
+            const float fac = m1 == m ? 1.0f : __builtin_amdgcn_exp2f(m - m1);
+            m = m1;
+            l *= fac;
+            limit = m == -__builtin_inff() ? m : (m + kSlack) / c;
+            offset = m == -__builtin_inff() ? 0.0f : -m;
+            if (lh == 0) sh.fac[(t & 1) * kSplitRows + row] = fac;
+            if (lane == 0) sh.raise[(t % 3) * 4 + wave] = 1;
+        }
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            float e[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) e[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[0][4 * g + j], c, offset));
+            l += (e[0] + e[1]) + (e[2] + e[3]);
+            *reinterpret_cast<u32x2 *>(pw + weight_unit(row, g) + 8 * lh) =
+                u32x2{dev::pack2<BF>(e[0], e[1]), dev::pack2<BF>(e[2], e[3])};
+        }
+    }
+    l = dev::sum_halves(l);
+    if (lh == 0) sh.sum[row] = l;
+    if (tile.steps) dev::lds_barrier();                   // the last step's probabilities
+}
+
+// Columns (V / 4) w .. of the summing wave w, all rows.  CAREFUL as in attend().
+template <bool BF, int NOPE, int V, bool CAREFUL>
+__device__ __forceinline__ bool sum_columns(const PromptArgs &a, const Tile &tile, const Shared &sh, uint32_t kv_lds, f32x16 (&acc)[V / 128][4]) {
+    using H = Head<NOPE, V>;
+    constexpr int kCols = V / 128;                        // 32-column blocks of the wave
+    const int lane = threadIdx.x & 63, wave = dev::wave_id() & 3, l31 = lane & 31, lh = lane >> 5;
+#pragma unroll
+    for (int cb = 0; cb < kCols; ++cb)
+#pragma unroll
+        for (int rb = 0; rb < 4; ++rb)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) acc[cb][rb][i] = 0.0f;
+    if (tile.steps == 0) return false;
+
+    // Copies: keys 8 w .. + 7 of a step, a 16-byte unit of every block per lane.
+    const int cr = 8 * wave + (lane >> 3), unit = ((lane & 7) ^ dev::tile_swz(cr)) << 4;
+    struct Copy {
+        const uint8_t *kv, *pe;
+        uint32_t dst;
+    };
+    auto aim = [&](int t) {
+        t = min(t, tile.steps - 1);                       // past the end the last step is copied again
+        const int64_t key = tile.k0 + min(t * kStepKeys + cr, tile.nk - 1);
+        return Copy{a.kv + (key * a.kv_tok + tile.head * a.kv_head) * 2 + unit, a.k_pe + key * a.pe_tok * 2 + unit,
+                    kv_lds + (t & (kRing - 1)) * H::kStepBytes + wave * 1024};
+    };
+    auto copy = [&](const Copy &x, int b) {
+        const uint8_t *src = b < H::kNopeBlocks ? x.kv + b * 128 : b == H::kNopeBlocks ? x.pe : x.kv + (b - 1) * 128;
+        dev::copy16_to_lds_free(src, x.dst + b * kBlockBytes);
+    };
+    auto copy_all = [&](const Copy &x) {
+#pragma unroll
+        for (int b = 0; b < H::kBlocks; ++b) copy(x, b);
+    };
+    const int vr = 8 * lh + ((lane >> 2) & 3);
+    auto step = [&](int t, bool more, Copy &now) {
+        const u32x4 raise = *reinterpret_cast<const u32x4 *>(sh.raise + (t % 3) * 4);
+        const uint8_t *pr = sh.p + (t & 1) * (kSplitRows * 64);
+        const uint8_t *vt = sh.kv + (t & (kRing - 1)) * H::kStepBytes + H::kKeyBlocks * kBlockBytes + 8 * (lane & 1);
+        u32x4 pf[2][4], vf[2][kCols];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+#pragma unroll
+            for (int cb = 0; cb < kCols; ++cb) {
+                const int col = wave * kCols + cb;        // 32-column block of the head's values
+                const uint8_t *blk = vt + (col >> 1) * kBlockBytes + 16 * k * 128;
+                const int u = 4 * (col & 1) + 2 * ((lane >> 4) & 1) + ((lane >> 1) & 1);
+                const u32x2 a0 = dev::read_tr(blk + dev::tile_unit(vr, u));
+                const u32x2 a1 = dev::read_tr(blk + dev::tile_unit(vr + 4, u));
+                vf[k][cb] = u32x4{a0[0], a0[1], a1[0], a1[1]};
             }
-            const bool masked = (t + 1) * kTileKeys > open;
-            if (masked) {
-                const int seen = (a.causal ? min(nk, row0 + row + ahead + 1) : nk) - t * kTileKeys - 4 * lh;
 #pragma unroll
-                for (int kb = 0; kb < 2; ++kb)
+            for (int rb = 0; rb < 4; ++rb) pf[k][rb] = *reinterpret_cast<const u32x4 *>(pr + weight_unit(32 * rb + l31, 2 * k + lh));
+        }
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        if (32 * kb + 8 * (i >> 2) + (i & 3) >= seen) s[kb][i] = -__builtin_inff();
+        for (int rb = 0; rb < 4; ++rb)
+            if (__builtin_amdgcn_readfirstlane(raise[rb])) {
+                const float f = sh.fac[(t & 1) * kSplitRows + 32 * rb + l31];
+#pragma unroll
+                for (int cb = 0; cb < kCols; ++cb)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) acc[cb][rb][i] *= f;
             }
-            float mx = s[0][0];
+        if (CAREFUL && (t + 1) * kStepKeys > seen_by(a, tile, 0)) {
+            const uint32_t one = BF ? 0x3F80u : 0x3C00u;
 #pragma unroll
-            for (int kb = 0; kb < 2; ++kb)
+            for (int cb = 0; cb < kCols; ++cb)
 #pragma unroll
-                for (int i = 0; i < 16; ++i) mx = fmaxf(mx, s[kb][i]);
-            mx = dev::max_halves(mx);
-            const float tm = mx * c;
-            const float m1 = tm > m + kSlack ? tm : m;
-            if (__any(m1 != m)) {
-                const float fac = m1 == m ? 1.0f : __builtin_amdgcn_exp2f(m - m1);
-                l *= fac;
-#pragma unroll
-                for (int cb = 0; cb < V / 32; ++cb)
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) acc[cb][i] *= fac;
-                m = m1;
-            }
-            const float ms = m1 == -__builtin_inff() ? 0.0f : m1;
-            u32x4 p[4];                                   // B operands of the four 16-key steps
-#pragma unroll
-            for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float e0 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[kb][2 * j], c, -ms));
-                    const float e1 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[kb][2 * j + 1], c, -ms));
-                    l += e0 + e1;
-                    p[2 * kb + (j >> 2)][j & 3] = dev::pack2<BF>(e0, e1);
-                }
-            // O^T: step k takes keys 16 k + 4 lh + 0..3 and 16 k + 8 + 4 lh + 0..3.
-            const uint8_t *vt = kv + kKeyBlocks * kBlockBytes;
-            const int vr = 4 * lh + ((lane >> 2) & 3);
-            auto value = [&](int k, int cb) {
-                const uint8_t *blk = vt + (cb >> 1) * kBlockBytes + 16 * k * 128 + 8 * (lane & 1);
-                const int unit = 4 * (cb & 1) + 2 * ((lane >> 4) & 1) + ((lane >> 1) & 1);
-                const u32x2 a0 = dev::read_tr(blk + dev::tile_unit(vr, unit));
-                const u32x2 a1 = dev::read_tr(blk + dev::tile_unit(vr + 8, unit));
-                return u32x4{a0[0], a0[1], a1[0], a1[1]};
-            };
-            if (!(careful && masked)) {
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-#pragma unroll
-                    for (int cb = 0; cb < V / 32; ++cb) acc[cb] = dev::mma<BF>(value(k, cb), p[k], acc[cb]);
-            } else {
-                // A hidden key's weight is zero, and zero times inf or NaN must
-                // not reach the row: values that are not finite are taken as
-                // zero, and a second product counts, per output, those that
-                // the row does see, which make that output NaN.
-                const int seen = (a.causal ? min(nk, row0 + row + ahead + 1) : nk) - t * kTileKeys - 4 * lh;
-                const uint32_t one = BF ? 0x3F80u : 0x3C00u;
-#pragma unroll
-                for (int cb = 0; cb < V / 32; ++cb) {
+                for (int rb = 0; rb < 4; ++rb) {
+                    const int seen = seen_by(a, tile, 32 * rb + l31) - t * kStepKeys - 8 * lh;
                     f32x16 n;
 #pragma unroll
                     for (int i = 0; i < 16; ++i) n[i] = 0.0f;
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        u32x4 v = value(k, cb), off, sees;
+                    for (int k = 0; k < 2; ++k) {
+                        u32x4 v = vf[k][cb], off, sees;
 #pragma unroll
                         for (int d = 0; d < 4; ++d) {
                             const uint32_t x = dev::nonfinite_halves<BF>(v[d]);
                             v[d] &= ~x;
                             off[d] = x & (one | one << 16);
-                            const int key = 16 * k + 8 * (d >> 1) + 2 * (d & 1);
-                            sees[d] = (key < seen ? one : 0u) | (key + 1 < seen ? one << 16 : 0u);
+                            const int at = 16 * k + 2 * d;
+                            sees[d] = (at < seen ? one : 0u) | (at + 1 < seen ? one << 16 : 0u);
                         }
-                        acc[cb] = dev::mma<BF>(v, p[k], acc[cb]);
+                        acc[cb][rb] = dev::mma<BF>(v, pf[k][rb], acc[cb][rb]);
                         n = dev::mma<BF>(off, sees, n);
                     }
 #pragma unroll
                     for (int i = 0; i < 16; ++i)
-                        if (n[i] > 0.0f) acc[cb][i] = __builtin_nanf("");
+                        if (n[i] > 0.0f) acc[cb][rb][i] = __builtin_nanf("");
                 }
-            }
+            if (more) copy_all(now);
+        } else {
+            // The copies are issued between the products.
+            int b = 0;
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+                for (int cb = 0; cb < kCols; ++cb)
+#pragma unroll
+                    for (int rb = 0; rb < 4; rb += 2) {
+                        __builtin_amdgcn_sched_barrier(0);
+                        if (more && b < H::kBlocks) copy(now, b++);
+                        __builtin_amdgcn_sched_barrier(0);
+                        acc[cb][rb] = dev::mma<BF>(vf[k][cb], pf[k][rb], acc[cb][rb]);
+                        acc[cb][rb + 1] = dev::mma<BF>(vf[k][cb], pf[k][rb + 1], acc[cb][rb + 1]);
+                    }
+            __builtin_amdgcn_sched_barrier(0);
+            if (more)
+#pragma unroll
+                for (; b < H::kBlocks; ++b) copy(now, b);
         }
-        float z = 0.0f;
-#pragma unroll
-        for (int cb = 0; cb < V / 32; ++cb)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) z = __builtin_fmaf(acc[cb][i], 0.0f, z);
-        dev::lds_barrier();
-        if (__any(z != 0.0f)) s_bad = 1;
-        dev::lds_barrier();
-        if (!s_bad) break;
-    }
+        if (more) now = aim(t + 4);
+    };
 
-    l = dev::sum_halves(l);
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-    const int64_t out_row = static_cast<int64_t>(q0 + row0 + row) * a.n_heads + head;
-    uint8_t *o = row < rows ? a.out + out_row * V * 2 : nullptr;
+    copy_all(aim(0));
+    copy_all(aim(1));
+    Copy now = aim(2);
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(H::kBlocks) : "memory");
+    dev::lds_barrier();
+    copy_all(now);
+    now = aim(3);
+    for (int t = 1; t < tile.steps; ++t) {
+        // Step t has landed when only the copies of step t + 1 are in flight.
+        asm volatile("s_waitcnt vmcnt(%0)" ::"n"(H::kBlocks) : "memory");
+        dev::lds_barrier();
+        step(t - 1, true, now);
+    }
+    dev::copy_barrier();
+    step(tile.steps - 1, false, now);
+    float z = 0.0f;
 #pragma unroll
-    for (int cb = 0; cb < V / 32; ++cb) dev::store_tile16<BF>(acc[cb], inv, o ? o + 64 * cb : nullptr);
-    if (a.lse && lh == 0 && row < rows)
-        a.lse[out_row] = l == 0.0f ? -__builtin_inff() : (m + __builtin_amdgcn_logf(l)) * kLn2;
+    for (int cb = 0; cb < kCols; ++cb)
+#pragma unroll
+        for (int rb = 0; rb < 4; ++rb)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) z = __builtin_fmaf(acc[cb][rb][i], 0.0f, z);
+    return __any(z != 0.0f);
+}
+
+template <bool BF, int NOPE, int V>
+__global__ __launch_bounds__(kSplitThreads, 2) void latent_prompt_split_kernel(PromptArgs a, int tiles_cap) {
+    __shared__ __align__(1024) uint8_t s_kv[kRing * Head<NOPE, V>::kStepBytes];
+    __shared__ __align__(1024) uint8_t s_p[2 * kSplitRows * 64];
+    __shared__ float s_fac[2 * kSplitRows], s_sum[kSplitRows];
+    __shared__ __align__(16) int s_raise[12];
+    __shared__ int s_bad;
+    const int tid = threadIdx.x, lane = tid & 63, wave = dev::wave_id();
+    const int l31 = lane & 31;
+    const uint32_t kv_lds = dev::lds_address(s_kv);
+    Tile tile;
+    if (!find_tile<kSplitRows>(a, tiles_cap, tile)) return;
+    const Shared sh{s_kv, s_p, s_fac, s_sum, s_raise};
+    const int64_t first = static_cast<int64_t>(tile.q0 + tile.row0) * a.n_heads + tile.head;
+    if (tid == 0) s_bad = 0;
+    if (tid < 12) s_raise[tid] = 0;
+    dev::lds_barrier();
+    if (wave < 4) {
+        float m;
+        score_rows<BF, NOPE, V>(a, tile, sh, m);
+        dev::lds_barrier();
+        if (s_bad) {                                      // the same scores again for the careful sums
+            dev::lds_barrier();
+            score_rows<BF, NOPE, V>(a, tile, sh, m);
+            dev::lds_barrier();
+        }
+        const int row = 32 * wave + l31;
+        const float l = s_sum[row];
+        if (a.lse && lane < 32 && row < tile.rows)
+            a.lse[first + static_cast<int64_t>(row) * a.n_heads] = l == 0.0f ? -__builtin_inff() : (m + __builtin_amdgcn_logf(l)) * kLn2;
+    } else {
+        f32x16 acc[V / 128][4];                           // [32 columns][32 rows] blocks of O^T
+        if (sum_columns<BF, NOPE, V, false>(a, tile, sh, kv_lds, acc)) s_bad = 1;
+        dev::lds_barrier();
+        if (s_bad) {
+            if (lane < 12) s_raise[lane] = 0;
+            dev::lds_barrier();
+            sum_columns<BF, NOPE, V, true>(a, tile, sh, kv_lds, acc);
+            dev::lds_barrier();
+        }
+#pragma unroll
+        for (int rb = 0; rb < 4; ++rb) {
+            const int row = 32 * rb + l31;
+            const float l = s_sum[row], inv = l == 0.0f ? 0.0f : 1.0f / l;
+            uint8_t *o = row < tile.rows ? a.out + ((first + static_cast<int64_t>(row) * a.n_heads) * V + (wave & 3) * (V / 4)) * 2 : nullptr;
+#pragma unroll
+            for (int cb = 0; cb < V / 128; ++cb) dev::store_tile16<BF>(acc[cb][rb], inv, o ? o + 64 * cb : nullptr);
+        }
+    }
+}
+
+// Row tiles of a call, an upper bound (every sequence may end in a part of
+// one), and the workgroups for them, a multiple of the XCDs.
+template <typename K>
+hipError_t launch_tiles(const PromptArgs &a, K kernel, int rows, int threads, hipStream_t s) {
+    const int64_t cap = std::min<int64_t>(a.n_q, a.n_q / rows + a.n_seq);
+    const int64_t grid = (cap * a.n_heads + 7) / 8 * 8;
+    if (grid > INT32_MAX) return hipErrorInvalidValue;
+    launch(kernel, static_cast<unsigned>(grid), threads, 0, s, a, static_cast<int>(cap));
+    return hipGetLastError();
 }
 
 template <bool BF>
-hipError_t launch_typed(const PromptArgs &a, int nope, unsigned grid, int cap, hipStream_t s) {
-    if (nope == 192) launch(latent_prompt_kernel<BF, 192, 256>, grid, 64 * kWaves, 0, s, a, cap);
-    else launch(latent_prompt_kernel<BF, 128, 128>, grid, 64 * kWaves, 0, s, a, cap);
-    return hipGetLastError();
+hipError_t launch_typed(const PromptArgs &a, int nope, hipStream_t s) {
+    if (nope == 192) return launch_tiles(a, latent_prompt_split_kernel<BF, 192, 256>, kSplitRows, kSplitThreads, s);
+    return launch_tiles(a, latent_prompt_kernel<BF, 128, 128>, kRows, 64 * kWaves, s);
 }
 
 }  // namespace
 
 hipError_t launch_latent_prompt(const PromptArgs &a, bool bf16, int nope, hipStream_t s) {
-    // Every sequence may end in a part of a tile: an upper bound of the tiles.
-    const int64_t cap = std::min<int64_t>(a.n_q, a.n_q / kRows + a.n_seq);
-    const int64_t grid = (cap * a.n_heads + 7) / 8 * 8;
-    if (grid > INT32_MAX) return hipErrorInvalidValue;
-    return bf16 ? launch_typed<true>(a, nope, static_cast<unsigned>(grid), static_cast<int>(cap), s)
-                : launch_typed<false>(a, nope, static_cast<unsigned>(grid), static_cast<int>(cap), s);
+    return bf16 ? launch_typed<true>(a, nope, s) : launch_typed<false>(a, nope, s);
 }
 
 }  // namespace coli
