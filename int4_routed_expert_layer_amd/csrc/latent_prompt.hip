@@ -6,9 +6,9 @@
 // are read where the up-projection left them ([token][head][nope + v]) and the
 // rotary part from its own rows, so no key is ever assembled in memory.
 //
-// A 512-thread workgroup (two waves per SIMD) takes 256 query rows of one head,
-// 32 per wave, and walks the keys in steps of 32 that are copied straight into
-// LDS, a ring of four.  S^T = K Q^T leaves lane L with row L % 32 of its wave
+// The narrow head: a wave takes 32 query rows of one head and walks the keys in
+// steps of 32 that its workgroup copies straight into LDS, a ring of three; two
+// waves share a SIMD.  S^T = K Q^T leaves lane L with row L % 32 of its wave
 // and half of the keys; rounded to 16 bits those registers are the second
 // product's B operand as they stand, because the order of keys inside a K step
 // is free as long as V^T (transposed LDS reads) takes them in the same order.
@@ -25,11 +25,10 @@ using dev::u32x4;
 
 constexpr int kStepKeys = 32;
 constexpr int kBlockBytes = kStepKeys * 128;
-constexpr int kRing = 4;
+constexpr int kRing = 4;          // of the wide head, whose values are read a step later
 constexpr float kSlack = 8.0f;    // see latent_decode.hip
 constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.69314718055994531f;
-constexpr int kWaves = 8;
-constexpr int kRows = 32 * kWaves;
+constexpr int kSlots = 3;         // ring of the narrow head: steps t, t + 1 and t + 2
 constexpr int kAhead = 4;         // LDS reads in flight ahead of the products that use them
 
 // The widths of one head, in 64-column blocks of the LDS step.
@@ -59,7 +58,7 @@ __device__ __forceinline__ int seen_by(const PromptArgs &a, const Tile &t, int r
 // that are not finite are taken as zero where a step hides keys, and a second
 // product counts, per output, those that the row does see, which make that
 // output NaN.
-template <bool BF, int NOPE, int V, bool CAREFUL>
+template <bool BF, int NOPE, int V, int WAVES, bool CAREFUL>
 __device__ __forceinline__ void attend(const PromptArgs &a, const Tile &tile, uint8_t *s_kv, uint32_t kv_lds, f32x16 (&acc)[V / 32],
                                        float &m, float &l) {
     using H = Head<NOPE, V>;
@@ -78,28 +77,25 @@ __device__ __forceinline__ void attend(const PromptArgs &a, const Tile &tile, ui
         for (int k = 0; k < H::kDepth; ++k) q[k] = dev::gload<u32x4>(src + 32 * k);
     }
 
-    // Copies.  A step is kBlocks x 32 rows x 128 bytes: piece i of it is rows
-    // 8 (i % 4) .. + 7 of block i / 4, one copy of a wave; wave w takes
-    // those rows w % 4 of every other block.
-    constexpr int kPieces = H::kBlocks * 4, kMine = (kPieces + kWaves - 1) / kWaves;
+    // Copies: wave w takes keys 8 (w % 4) .. + 7 of a step, a 16-byte unit per
+    // lane of every block, or with eight waves of every other block.
+    constexpr int kShare = WAVES / 4, kMost = (H::kBlocks + kShare - 1) / kShare;
+    const int part = wave >> 2, mine = (H::kBlocks - part + kShare - 1) / kShare;
+    const int cr = 8 * (wave & 3) + (lane >> 3), unit = ((lane & 7) ^ dev::tile_swz(cr)) << 4;
     auto copy_step = [&](int t) {
+        const uint32_t dst = kv_lds + (t % kSlots) * H::kStepBytes + (wave & 3) * 1024;
         t = min(t, tile.steps - 1);                       // past the end the last step is copied again
-        const int cr = 8 * (wave & 3) + (lane >> 3);
         const int64_t key = tile.k0 + min(t * kStepKeys + cr, tile.nk - 1);
-        const int unit = ((lane & 7) ^ dev::tile_swz(cr)) << 4;
         const uint8_t *kv = a.kv + (key * a.kv_tok + tile.head * a.kv_head) * 2 + unit;
         const uint8_t *pe = a.k_pe + key * a.pe_tok * 2 + unit;
-        const uint32_t dst = kv_lds + (t & (kRing - 1)) * H::kStepBytes + (wave & 3) * 1024;
 #pragma unroll
-        for (int i = 0; i < kMine; ++i) {
-            const int b = 2 * i + (wave >> 2);            // blocks 0, 2, .. or 1, 3, ..
-            if (H::kBlocks % 2 && i == kMine - 1 && b >= H::kBlocks) break;
+        for (int i = 0; i < kMost; ++i) {
+            const int b = kShare * i + part;
+            if (b >= H::kBlocks) break;
             const uint8_t *src = b < H::kNopeBlocks ? kv + b * 128 : b == H::kNopeBlocks ? pe : kv + (b - 1) * 128;
             dev::copy16_to_lds(src, dst + b * kBlockBytes);
         }
     };
-    // Copies of a wave per step, the same for every step.
-    const int each = H::kBlocks % 2 ? kMine - (wave >> 2) : kMine;
 
 #pragma unroll
     for (int cb = 0; cb < V / 32; ++cb)
@@ -113,14 +109,14 @@ __device__ __forceinline__ void attend(const PromptArgs &a, const Tile &tile, ui
     copy_step(1);
     for (int t = 0; t < tile.steps; ++t) {
         // Step t has landed when only the copies of step t + 1 are in flight.
-        if (H::kBlocks % 2 == 0 || each == kMine)
-            asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kMine) : "memory");
+        if (mine == kMost)
+            asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kMost) : "memory");
         else
-            asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kMine - 1) : "memory");
+            asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kMost - 1) : "memory");
         dev::lds_barrier();
         copy_step(t + 2);
         if (t * kStepKeys >= shut) continue;
-        const uint8_t *kv = s_kv + (t & (kRing - 1)) * H::kStepBytes;
+        const uint8_t *kv = s_kv + (t % kSlots) * H::kStepBytes;
         auto key = [&](int k) { return *reinterpret_cast<const u32x4 *>(kv + (k >> 2) * kBlockBytes + dev::tile_unit(l31, 2 * (k & 3) + lh)); };
         f32x16 s;
 #pragma unroll
@@ -237,13 +233,16 @@ __device__ __forceinline__ bool find_tile(const PromptArgs &a, int tiles_cap, Ti
     const int want = tiles_cap - 1 - (lin - tile.head * tiles_cap);
     // Sequence and row tile number `want` of the call: each lane counts one
     // sequence's tiles.
-    int seq = -1, number = 0;
-    bool bad_seq = false;
+    int number = 0, nq = 0;
+    bool found = false, bad_seq = false;
     for (int b0 = 0, done = 0; b0 < a.n_seq; b0 += 64) {
         const int b = b0 + lane;
-        int n = 0;
+        int n = 0, q0 = 0, q1 = 0, k0 = 0, k1 = 0;
         if (b < a.n_seq) {
-            const int q0 = a.q_start[b], q1 = a.q_start[b + 1];
+            q0 = a.q_start[b];
+            q1 = a.q_start[b + 1];
+            k0 = a.k_start[b];
+            k1 = a.k_start[b + 1];
             if (q0 >= 0 && q1 >= q0 && q1 <= a.n_q) n = (q1 - q0 + ROWS - 1) / ROWS;
             else bad_seq = true;
         }
@@ -256,20 +255,18 @@ __device__ __forceinline__ bool find_tile(const PromptArgs &a, int tiles_cap, Ti
         const uint64_t hit = __ballot(done + cum > want);
         if (hit) {
             const int at = __ffsll(static_cast<unsigned long long>(hit)) - 1;
-            seq = b0 + at;
-            number = want - done - (__shfl(cum, at, 64) - __shfl(n, at, 64));
+            found = true;
+            number = want - done - (__builtin_amdgcn_readlane(cum, at) - __builtin_amdgcn_readlane(n, at));
+            tile.q0 = __builtin_amdgcn_readlane(q0, at);
+            nq = __builtin_amdgcn_readlane(q1, at) - tile.q0;
+            tile.k0 = __builtin_amdgcn_readlane(k0, at);
+            tile.nk = __builtin_amdgcn_readlane(k1, at) - tile.k0;
             break;
         }
-        done += __shfl(cum, 63, 64);
+        done += __builtin_amdgcn_readlane(cum, 63);
     }
     dev::flag_if(bad_seq, a.err, kErrSeq);
-    seq = __builtin_amdgcn_readfirstlane(seq);
-    number = __builtin_amdgcn_readfirstlane(number);
-    if (seq < 0) return false;
-    tile.q0 = dev::ld_uniform(a.q_start + seq);
-    const int nq = dev::ld_uniform(a.q_start + seq + 1) - tile.q0;
-    tile.k0 = dev::ld_uniform(a.k_start + seq);
-    tile.nk = dev::ld_uniform(a.k_start + seq + 1) - tile.k0;
+    if (!found) return false;
     if (tile.k0 < 0 || tile.nk < 0 || tile.nk > a.n_k - tile.k0) {
         dev::flag_if(threadIdx.x == 0, a.err, kErrSeq);
         tile.k0 = tile.nk = 0;
@@ -282,20 +279,20 @@ __device__ __forceinline__ bool find_tile(const PromptArgs &a, int tiles_cap, Ti
     return true;
 }
 
-template <bool BF, int NOPE, int V>
-__global__ __launch_bounds__(64 * kWaves, 2) void latent_prompt_kernel(PromptArgs a, int tiles_cap) {
-    __shared__ __align__(1024) uint8_t s_kv[kRing * Head<NOPE, V>::kStepBytes];
+template <bool BF, int NOPE, int V, int WAVES>
+__global__ __launch_bounds__(64 * WAVES, 2) void latent_prompt_kernel(PromptArgs a, int tiles_cap) {
+    __shared__ __align__(1024) uint8_t s_kv[kSlots * Head<NOPE, V>::kStepBytes];
     __shared__ int s_bad;
     const int tid = threadIdx.x, lane = tid & 63, wave = dev::wave_id();
     const int l31 = lane & 31, lh = lane >> 5;
     const uint32_t kv_lds = dev::lds_address(s_kv);
     Tile tile;
-    if (!find_tile<kRows>(a, tiles_cap, tile)) return;
+    if (!find_tile<32 * WAVES>(a, tiles_cap, tile)) return;
 
     f32x16 acc[V / 32];                                   // [32 columns][32 rows] blocks of O^T
     float m, l;
     if (tid == 0) s_bad = 0;
-    attend<BF, NOPE, V, false>(a, tile, s_kv, kv_lds, acc, m, l);
+    attend<BF, NOPE, V, WAVES, false>(a, tile, s_kv, kv_lds, acc, m, l);
     // Anything that is not finite: again with care, if a step hides keys.
     float z = 0.0f;
 #pragma unroll
@@ -305,7 +302,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void latent_prompt_kernel(PromptArg
     dev::lds_barrier();
     if (__any(z != 0.0f)) s_bad = 1;
     dev::lds_barrier();
-    if (s_bad) attend<BF, NOPE, V, true>(a, tile, s_kv, kv_lds, acc, m, l);
+    if (s_bad) attend<BF, NOPE, V, WAVES, true>(a, tile, s_kv, kv_lds, acc, m, l);
 
     const int row = 32 * wave + l31;
     l = dev::sum_halves(l);
@@ -626,7 +623,7 @@ hipError_t launch_tiles(const PromptArgs &a, K kernel, int rows, int threads, hi
 template <bool BF>
 hipError_t launch_typed(const PromptArgs &a, int nope, hipStream_t s) {
     if (nope == 192) return launch_tiles(a, latent_prompt_split_kernel<BF, 192, 256>, kSplitRows, kSplitThreads, s);
-    return launch_tiles(a, latent_prompt_kernel<BF, 128, 128>, kRows, 64 * kWaves, s);
+    return launch_tiles(a, latent_prompt_kernel<BF, 128, 128, 4>, 128, 256, s);
 }
 
 }  // namespace
