@@ -26,8 +26,17 @@ using dev::u32x2;
 using dev::u32x4;
 
 constexpr int kSampleThreads = 256, kWalkThreads = 1024;
-constexpr int kSliceMost = 16384;      // elements of a slice: a bit each for the refused tokens
-constexpr int kSliceLeast = 2048;
+// A workgroup takes its slice of a row in chunks of four groups of four elements
+// per thread, all in flight at once; the first of race is loaded before the
+// walk, which says which row of p it meets.  Slices are one to four chunks,
+// as many as let every workgroup (five fit a CU) start at once: each makes the
+// walk again.  64 sequences of 151643 probabilities: two chunks 19.8 us; one
+// chunk (two rounds of workgroups) 31.5 us; 16384 elements in 16 rounds of one
+// group 24.3 us.
+constexpr int kGroups = 4;
+constexpr int kChunk = kSampleThreads * 4 * kGroups;
+constexpr int kMostChunks = 4;
+constexpr int kPerCU = 5;
 
 enum Kind { kF32 = COLI_PROB_F32, kBF16 = COLI_PROB_BF16, kF16 = COLI_PROB_F16 };
 
@@ -263,12 +272,24 @@ __device__ __forceinline__ uint64_t candidate(float score, int i) {
 }
 
 template <int K, bool WALKED>
-__global__ __launch_bounds__(kSampleThreads) void sample_kernel(VerifyArgs a, int slice) {
+__global__ __launch_bounds__(kSampleThreads, kPerCU) void sample_kernel(VerifyArgs a, int chunks) {
     __shared__ Nodes s;
-    __shared__ uint32_t s_gone[kSliceMost / 32];
+    __shared__ uint32_t s_gone[kMostChunks * kChunk / 32];   // bits of the refused tokens
     __shared__ uint64_t s_best[2][kSampleThreads / 64];
     const int seq = blockIdx.y, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const bool first = blockIdx.x == 0;
+    const int lo = blockIdx.x * chunks * kChunk, hi = min(lo + chunks * kChunk, a.vocab);
+    const float *race = a.race + seq * a.race_stride;
+    f32x4u g[kGroups];
+    auto load_race = [&](int c, f32x4u (&to)[kGroups]) {
+#pragma unroll
+        for (int k = 0; k < kGroups; ++k) {
+            const int i = lo + c * kChunk + 4 * (tid + k * kSampleThreads);
+            to[k] = f32x4u{0.0f, 0.0f, 0.0f, 0.0f};
+            if (i + 4 <= hi) to[k] = *reinterpret_cast<const f32x4u *>(race + i);
+        }
+    };
+    load_race(0, g);
     int t0, n, steps;
     bool bad = false;
     const bool ok = bounds(a, seq, t0, n);
@@ -291,10 +312,9 @@ __global__ __launch_bounds__(kSampleThreads) void sample_kernel(VerifyArgs a, in
         }
         steps = s.steps;
     }
-    const int lo = blockIdx.x * slice, hi = min(lo + slice, a.vocab);
     const bool remove = !WALKED && !a.q && w.refused > 0;   // refused tokens without draft rows
     if (remove) {
-        for (int i = tid; i < slice / 32; i += kSampleThreads) s_gone[i] = 0;
+        for (int i = tid; i < kMostChunks * kChunk / 32; i += kSampleThreads) s_gone[i] = 0;
         __syncthreads();
         for (int j = w.node + 1 + tid; j < n; j += kSampleThreads)
             if (s.parent[j] == w.node && s.x[j] >= lo && s.x[j] < hi)
@@ -303,7 +323,6 @@ __global__ __launch_bounds__(kSampleThreads) void sample_kernel(VerifyArgs a, in
     }
     const uint8_t *p = a.p + (t0 + w.node) * a.p_stride * prob_bytes<K>();
     const uint8_t *q = a.q ? a.q + (t0 + w.node) * a.q_stride * prob_bytes<K>() : nullptr;
-    const float *race = a.race + seq * a.race_stride;
     const bool drawn = q && w.refused > 0;
     // The best of the residual, and of p itself where the residual is nothing.
     uint64_t best = 0, whole = 0;
@@ -317,18 +336,34 @@ __global__ __launch_bounds__(kSampleThreads) void sample_kernel(VerifyArgs a, in
         const uint64_t c = candidate(pv * g, i);
         whole = c > whole ? c : whole;
     };
-    int i = lo + 4 * tid;
-    for (; i + 4 <= hi; i += 4 * kSampleThreads) {
-        float pv[4], qv[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        prob4<K>(p, i, pv);
-        if (drawn) prob4<K>(q, i, qv);
-        const f32x4u g = *reinterpret_cast<const f32x4u *>(race + i);
-        const uint32_t gone = remove ? s_gone[(i - lo) >> 5] >> ((i - lo) & 31) : 0u;
+    for (int c = 0; c < chunks; ++c) {
+        const int at = lo + c * kChunk;
+        float pv[kGroups][4], qv[kGroups][4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) one(i + j, pv[j], qv[j], g[j], (gone >> j) & 1);
+        for (int k = 0; k < kGroups; ++k) {
+            const int i = at + 4 * (tid + k * kSampleThreads);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) pv[k][j] = qv[k][j] = 0.0f;
+            if (i + 4 <= hi) {
+                prob4<K>(p, i, pv[k]);
+                if (drawn) prob4<K>(q, i, qv[k]);
+            }
+        }
+        if (c > 0) load_race(c, g);
+#pragma unroll
+        for (int k = 0; k < kGroups; ++k) {
+            const int i = at + 4 * (tid + k * kSampleThreads);
+            if (i >= hi) continue;
+            const uint32_t gone = remove ? s_gone[(i - lo) >> 5] >> ((i - lo) & 31) : 0u;
+            if (i + 4 <= hi) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) one(i + j, pv[k][j], qv[k][j], g[k][j], (gone >> j) & 1);
+            } else {
+                for (int j = 0; i + j < hi; ++j)
+                    one(i + j, prob<K>(p, i + j), drawn ? prob<K>(q, i + j) : 0.0f, race[i + j], (gone >> j) & 1);
+            }
+        }
     }
-    for (; i < hi; ++i)
-        one(i, prob<K>(p, i), drawn ? prob<K>(q, i) : 0.0f, race[i], remove && ((s_gone[(i - lo) >> 5] >> ((i - lo) & 31)) & 1));
 #pragma unroll
     for (int o = 32; o; o >>= 1) {
         const uint64_t x = __shfl_xor(static_cast<unsigned long long>(best), o, 64);
@@ -360,21 +395,17 @@ __global__ __launch_bounds__(kSampleThreads) void sample_kernel(VerifyArgs a, in
 
 template <int K>
 hipError_t launch_kind(const VerifyArgs &a, int n_cu, hipStream_t s) {
-    // Slices: enough workgroups for two per CU, none under kSliceLeast
-    // elements nor over what the refused-token bits hold.
-    const int want = std::max(1, 2 * n_cu / a.n_seq);
-    int slice = (a.vocab + want - 1) / want;
-    slice = std::min(std::max(slice, kSliceLeast), kSliceMost);
-    slice = (slice + 1023) / 1024 * 1024;
-    const unsigned slices = static_cast<unsigned>((a.vocab + slice - 1) / slice);
+    const int64_t want = (static_cast<int64_t>(a.vocab) * a.n_seq + static_cast<int64_t>(kPerCU) * n_cu * kChunk - 1) / (static_cast<int64_t>(kPerCU) * n_cu * kChunk);
+    const int chunks = static_cast<int>(std::min<int64_t>(std::max<int64_t>(want, 1), kMostChunks));
+    const unsigned slices = static_cast<unsigned>((a.vocab + chunks * kChunk - 1) / (chunks * kChunk));
     const bool sums = a.q && a.parents;
     if (sums) {
         launch(walk_kernel<K>, static_cast<unsigned>(a.n_seq), kWalkThreads, 0, s, a);
         hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
-        launch(sample_kernel<K, true>, dim3(slices, a.n_seq), kSampleThreads, 0, s, a, slice);
+        launch(sample_kernel<K, true>, dim3(slices, a.n_seq), kSampleThreads, 0, s, a, chunks);
     } else {
-        launch(sample_kernel<K, false>, dim3(slices, a.n_seq), kSampleThreads, 0, s, a, slice);
+        launch(sample_kernel<K, false>, dim3(slices, a.n_seq), kSampleThreads, 0, s, a, chunks);
     }
     return hipGetLastError();
 }
