@@ -95,6 +95,7 @@ struct Shared {
 // such a key has a NaN score.)
 template <bool BF>
 __device__ __forceinline__ void clean(const Shared &sh, int t) {
+    dev::lds_barrier();                                  // no copy is in flight, and every wave has read the step's keys
     u32x4 *v = reinterpret_cast<u32x4 *>(sh.ring(t));
     for (int i = threadIdx.x; i < kLatentBlocks * kBlockBytes / 16; i += kThreads) {
         u32x4 w = v[i];
@@ -373,12 +374,11 @@ __device__ __forceinline__ void sum_item(const DecodeArgs &a, const DecodeItem &
 
     const int pg0 = page_of(sh.t0), pg1 = page_of(sh.t0 + 1), pg2 = page_of(sh.t0 + 2), pg3 = page_of(sh.t0 + 3);
     int page = page_of(sh.t0 + 4);
-    copy_all(aim(sh.t0, pg0));
-    copy_all(aim(sh.t0 + 1, pg1));
-    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kBlocks) : "memory");
-    dev::lds_barrier();                                  // step t0 has landed
-    copy_all(aim(sh.t0 + 2, pg2));
+#pragma unroll 1
+    for (int i = 0; i < 3; ++i) copy_all(aim(sh.t0 + i, i == 0 ? pg0 : i == 1 ? pg1 : pg2));
     Copy now = aim(sh.t0 + 3, pg3);
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * kBlocks) : "memory");
+    dev::lds_barrier();                                  // step t0 has landed
     dev::lds_barrier();                                  // the first maxima
     for (int t = sh.t0 + 1; t < sh.t1; ++t) {
         // Step t has landed when only the copies of step t + 1 are in flight.
@@ -479,18 +479,17 @@ __global__ __launch_bounds__(kThreads, 2) void latent_decode_kernel(DecodeArgs a
                     dev::store_tile16<BF>(acc[cb][1], i1, 32 + l31 < rows ? o + 32 * kLatent * 2 : nullptr);
                 }
             } else {
-                float *part = a.part + static_cast<int64_t>(it.slot) * kTileRows * kLatent;
+                // Sixteen bytes per lane, a wave's 1 KB together (rows would
+                // spread each store over 32 of them).
+                f32x4 *part = reinterpret_cast<f32x4 *>(a.part + static_cast<int64_t>(it.slot) * kTileRows * kLatent) + w * 32 * 64 + lane;
 #pragma unroll
                 for (int cb = 0; cb < 4; ++cb)
 #pragma unroll
                     for (int rb = 0; rb < 2; ++rb)
-                        if (32 * rb + l31 < rows) {
-                            float *o = part + (32 * rb + l31) * kLatent + 128 * w + 32 * cb + 4 * lh;
 #pragma unroll
-                            for (int g = 0; g < 4; ++g)
-                                *reinterpret_cast<f32x4 *>(o + 8 * g) = f32x4{acc[cb][rb][4 * g], acc[cb][rb][4 * g + 1],
-                                                                              acc[cb][rb][4 * g + 2], acc[cb][rb][4 * g + 3]};
-                        }
+                        for (int g = 0; g < 4; ++g)
+                            part[((cb * 2 + rb) * 4 + g) * 64] = f32x4{acc[cb][rb][4 * g], acc[cb][rb][4 * g + 1],
+                                                                       acc[cb][rb][4 * g + 2], acc[cb][rb][4 * g + 3]};
             }
         }
         dev::flag_if(bad_page, a.err, kErrPage);
@@ -498,77 +497,71 @@ __global__ __launch_bounds__(kThreads, 2) void latent_decode_kernel(DecodeArgs a
 }
 
 // Joins the pieces of a row: with M = max m_i, o = sum 2^(m_i - M) O_i / sum
-// 2^(m_i - M) l_i, summed in a fixed order.  Each lane of a wave holds one
-// piece's factor, so the statistics are one load, and eight columns.  Up to
-// kWavePieces pieces a wave joins a row by itself (four rows a workgroup, all
-// partial rows in flight together); more of them are shared by the four
-// waves of a workgroup and added up in LDS.
+// 2^(m_i - M) l_i, summed in a fixed order.  A piece is 32 blocks of 4 KB as the
+// summing waves held them: block (w 4 + cb) 2 + rb is rows 32 rb .. + 31 of
+// columns 128 w + 32 cb .. + 31 as an accumulator, sixteen bytes of each lane at
+// a time.  A wave joins one block of up to kWavePieces pieces, all of them in
+// flight; of more the four waves of a workgroup take a quarter each and add up
+// in LDS.
 constexpr int kWavePieces = 8;
+constexpr int kOutBlocks = kTileRows * kLatent / 1024;
 
 template <bool BF>
 __global__ __launch_bounds__(256) void join_kernel(DecodeArgs a) {
-    __shared__ float s_o[4][kLatent];
-    __shared__ float s_l[4];
+    __shared__ f32x4 s_o[3][4][64];
+    __shared__ float s_l[3][64];
     const int joins = dev::ld_uniform(a.plan.head), most = dev::ld_uniform(a.plan.head + 1);
     const bool apart = most <= kWavePieces;
-    const int per = apart ? kTileRows / 4 : kTileRows;
+    const int per = apart ? kOutBlocks / 4 : kOutBlocks;
     const int lane = threadIdx.x & 63, wave = dev::wave_id();
-    for (int w = blockIdx.x; w < joins * per; w += gridDim.x) {
-        const JoinUnit u = a.plan.joins[w / per];
-        const int r = apart ? 4 * (w % per) + wave : w % per;
-        if (apart ? r >= u.rows : w % per >= u.rows) continue;
-        const float *ml = a.part_ml + (static_cast<int64_t>(u.slot0) * kTileRows + r) * 2;
-        const float *part = a.part + (static_cast<int64_t>(u.slot0) * kTileRows + r) * kLatent + 4 * lane;
+    for (int wg = blockIdx.x; wg < joins * per; wg += gridDim.x) {
+        const JoinUnit u = a.plan.joins[wg / per];
+        const int block = apart ? 4 * (wg % per) + wave : wg % per;
+        const int r = 32 * (block & 1) + (lane & 31);
+        const bool live = r < u.rows;                     // partial rows past the unit's hold no statistics
+        const float *ml = a.part_ml + (static_cast<int64_t>(u.slot0) * kTileRows + (live ? r : 0)) * 2;
+        const f32x4 *part = reinterpret_cast<const f32x4 *>(a.part + static_cast<int64_t>(u.slot0) * kTileRows * kLatent) + block * 256 + lane;
         float top = -__builtin_inff();
-        for (int i = lane; i < u.split; i += 64) top = fmaxf(top, ml[i * kTileRows * 2]);
-#pragma unroll
-        for (int o = 32; o; o >>= 1) top = fmaxf(top, __shfl_xor(top, o, 64));
+#pragma unroll 8
+        for (int i = 0; i < u.split; ++i) top = fmaxf(top, ml[i * kTileRows * 2]);
         const float ms = top == -__builtin_inff() ? 0.0f : top;
         float l = 0.0f;
-        f32x4 o[2] = {f32x4{0.0f, 0.0f, 0.0f, 0.0f}, f32x4{0.0f, 0.0f, 0.0f, 0.0f}};
-        // This wave's pieces: all, or a quarter.
+        f32x16 o;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[i] = 0.0f;
         const int p0 = apart ? 0 : u.split * wave / 4, p1 = apart ? u.split : u.split * (wave + 1) / 4;
-        for (int i0 = p0; i0 < p1; i0 += 64) {
-            const int here = min(64, p1 - i0);
-            const float *mine = ml + static_cast<int64_t>(i0 + min(lane, here - 1)) * kTileRows * 2;
-            const float f = lane < here ? __builtin_amdgcn_exp2f(mine[0] - ms) : 0.0f;
-            float sum = lane < here ? f * mine[1] : 0.0f;
+#pragma unroll 4
+        for (int i = p0; i < p1; ++i) {
+            const float f = __builtin_amdgcn_exp2f(ml[i * kTileRows * 2] - ms);
+            l = __builtin_fmaf(f, ml[i * kTileRows * 2 + 1], l);
 #pragma unroll
-            for (int d = 32; d; d >>= 1) sum += __shfl_xor(sum, d, 64);
-            l += sum;
-#pragma unroll 8
-            for (int i = 0; i < here; ++i) {
-                const float fi = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(f), i));
-                const float *x = part + static_cast<int64_t>(i0 + i) * kTileRows * kLatent;
+            for (int g = 0; g < 4; ++g) {
+                const f32x4 v = part[static_cast<int64_t>(i) * (kTileRows * kLatent / 4) + 64 * g];
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const f32x4 v = *reinterpret_cast<const f32x4 *>(x + 256 * h);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) o[h][j] = __builtin_fmaf(fi, v[j], o[h][j]);
-                }
+                for (int j = 0; j < 4; ++j) o[4 * g + j] = __builtin_fmaf(f, v[j], o[4 * g + j]);
             }
         }
         if (!apart) {
             __syncthreads();
+            if (wave) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) *reinterpret_cast<f32x4 *>(&s_o[wave][4 * lane + 256 * h]) = o[h];
-            if (lane == 0) s_l[wave] = l;
+                for (int g = 0; g < 4; ++g) s_o[wave - 1][g][lane] = f32x4{o[4 * g], o[4 * g + 1], o[4 * g + 2], o[4 * g + 3]};
+                s_l[wave - 1][lane] = l;
+            }
             __syncthreads();
-            if (wave != 0) continue;
+            if (wave) continue;
 #pragma unroll
-            for (int k = 1; k < 4; ++k) {
-                l += s_l[k];
+            for (int k = 0; k < 3; ++k) {
+                l += s_l[k][lane];
 #pragma unroll
-                for (int h = 0; h < 2; ++h) o[h] += *reinterpret_cast<const f32x4 *>(&s_o[k][4 * lane + 256 * h]);
+                for (int g = 0; g < 4; ++g)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) o[4 * g + j] += s_o[k][g][lane][j];
             }
         }
-        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
         const int64_t row = u.out_row + r;
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-            *reinterpret_cast<u32x2 *>(a.out + (row * kLatent + 4 * lane + 256 * h) * 2) =
-                u32x2{dev::pack2<BF>(o[h][0] * inv, o[h][1] * inv), dev::pack2<BF>(o[h][2] * inv, o[h][3] * inv)};
-        if (a.lse && lane == 0) a.lse[row] = l == 0.0f ? -__builtin_inff() : (top + __builtin_amdgcn_logf(l)) * kLn2;
+        dev::store_tile16<BF>(o, l == 0.0f ? 0.0f : 1.0f / l, live ? a.out + (row * kLatent + 32 * (block >> 1)) * 2 : nullptr);
+        if (a.lse && block < 2 && lane < 32 && live) a.lse[row] = l == 0.0f ? -__builtin_inff() : (top + __builtin_amdgcn_logf(l)) * kLn2;
     }
 }
 
@@ -737,7 +730,7 @@ hipError_t launch_latent_decode(const DecodeArgs &a, bool bf16, int n_cu, hipStr
     launch(bf16 ? latent_decode_kernel<true> : latent_decode_kernel<false>, static_cast<unsigned>(n_cu), kThreads, 0, s, a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    const unsigned blocks = static_cast<unsigned>(std::min<int64_t>(static_cast<int64_t>(a.join_most) * kTileRows, 8 * n_cu));
+    const unsigned blocks = static_cast<unsigned>(std::min<int64_t>(static_cast<int64_t>(a.join_most) * kOutBlocks, 8 * n_cu));
     launch(bf16 ? join_kernel<true> : join_kernel<false>, blocks, 256u, 0, s, a);
     return hipGetLastError();
 }

@@ -63,7 +63,7 @@ struct DecodeArgs {
     float *lse;                // [n_tok x n_heads] or NULL
     DecodePlan plan;
     int join_most;             // at least the plan's join units
-    float *part;               // [slot_cap x 64 x 512]
+    float *part;               // [slot_cap x 64 x 512], in the order of join_kernel's blocks
     float *part_ml;            // [slot_cap x 64 x 2]
     int32_t *err;
 };
