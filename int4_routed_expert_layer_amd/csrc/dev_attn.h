@@ -115,6 +115,11 @@ __device__ __forceinline__ void copy16_to_lds_free(const void *src, uint32_t lds
     asm volatile("global_load_lds_dwordx4 %0, off" ::"v"(src), "{m0}"(lds_addr));
 }
 
+// The same for data read once (non-temporal).
+__device__ __forceinline__ void copy16_to_lds_once(const void *src, uint32_t lds_addr) {
+    asm volatile("global_load_lds_dwordx4 %0, off nt" ::"v"(src), "{m0}"(lds_addr));
+}
+
 // Workgroup barrier that waits for this wave's LDS accesses but not for its
 // global loads in flight (__syncthreads would).
 __device__ __forceinline__ void lds_barrier() {

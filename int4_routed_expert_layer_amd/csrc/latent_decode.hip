@@ -257,7 +257,7 @@ __device__ __forceinline__ void score_item(const DecodeArgs &a, const DecodeItem
 
 // The summing waves' part: wave w copies keys 8 w .. + 7 of each step and sums
 // columns 128 w .. + 127 for all rows.
-template <bool BF>
+template <bool BF, bool ONCE>
 __device__ __forceinline__ void sum_item(const DecodeArgs &a, const DecodeItem &it, const Shared &sh, uint32_t kv_lds, bool careful,
                                          bool &bad_page, f32x16 (&acc)[4][2]) {
     const int lane = threadIdx.x & 63, wave = dev::wave_id() & 3, l31 = lane & 31, lh = lane >> 5;
@@ -300,7 +300,10 @@ __device__ __forceinline__ void sum_item(const DecodeArgs &a, const DecodeItem &
         return Copy{a.cache.base + (page * a.cache.page_stride + static_cast<int64_t>(pos & ((1 << shift) - 1)) * kCacheRow) * 2 + cu,
                     kv_lds + ((t - sh.t0) & (kRing - 1)) * kStepBytes + wave * 1024};
     };
-    auto copy = [&](const Copy &x, int b) { dev::copy16_to_lds_free(x.src + b * 128, x.dst + b * kBlockBytes); };
+    auto copy = [&](const Copy &x, int b) {
+        if constexpr (ONCE) dev::copy16_to_lds_once(x.src + b * 128, x.dst + b * kBlockBytes);
+        else dev::copy16_to_lds_free(x.src + b * 128, x.dst + b * kBlockBytes);
+    };
     auto copy_all = [&](const Copy &x) {
 #pragma unroll
         for (int b = 0; b < kBlocks; ++b) copy(x, b);
@@ -411,7 +414,7 @@ __device__ __forceinline__ DecodeItem take_item(const DecodeArgs &a, int round, 
     return it;
 }
 
-template <bool BF>
+template <bool BF, bool ONCE>
 __global__ __launch_bounds__(kThreads, 2) void latent_decode_kernel(DecodeArgs a) {
     __shared__ __align__(1024) uint8_t s_kv[kRing * kStepBytes];
     __shared__ __align__(1024) uint8_t s_p[2 * kTileRows * 64];
@@ -464,7 +467,7 @@ __global__ __launch_bounds__(kThreads, 2) void latent_decode_kernel(DecodeArgs a
             f32x16 acc[4][2];                            // [32 columns][32 rows] blocks of O^T
             for (int careful = 0; careful < 2; ++careful) {
                 dev::lds_barrier();
-                sum_item<BF>(a, it, sh, kv_lds, careful, bad_page, acc);
+                sum_item<BF, ONCE>(a, it, sh, kv_lds, careful, bad_page, acc);
                 dev::lds_barrier();
                 if (!(s_bad && sh.t1 * kStepKeys > sh.open)) break;
             }
@@ -727,7 +730,15 @@ hipError_t launch_decode_plan(const DecodePlan &p, const int32_t *q_start, const
 }
 
 hipError_t launch_latent_decode(const DecodeArgs &a, bool bf16, int n_cu, hipStream_t s) {
-    launch(bf16 ? latent_decode_kernel<true> : latent_decode_kernel<false>, static_cast<unsigned>(n_cu), kThreads, 0, s, a);
+    // Where a sequence's rows fill one item (on the average: the sequences' own
+    // counts are the device's), its keys are read once and not kept in the
+    // caches: 64 sequences up to 12k tokens 88 -> 81 us.  Items that share keys
+    // lose by it (trees of 25 nodes 173 -> 178 us), and by a test at each
+    // copy instead of two kernels (191 us).
+    const bool once = static_cast<int64_t>(a.n_tok) * a.n_heads <= static_cast<int64_t>(a.n_seq) * kTileRows;
+    launch(once ? (bf16 ? latent_decode_kernel<true, true> : latent_decode_kernel<false, true>)
+                : (bf16 ? latent_decode_kernel<true, false> : latent_decode_kernel<false, false>),
+           static_cast<unsigned>(n_cu), kThreads, 0, s, a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     const unsigned blocks = static_cast<unsigned>(std::min<int64_t>(static_cast<int64_t>(a.join_most) * kOutBlocks, 8 * n_cu));

@@ -57,7 +57,7 @@ struct DecodeArgs {
     CacheView cache;
     const uint64_t *mask;      // [n_tok x mask_words] ancestor bits, or NULL for a chain
     int mask_words;
-    int n_heads;
+    int n_tok, n_seq, n_heads;
     float scale;
     uint8_t *out;              // [n_tok x n_heads x 512]
     float *lse;                // [n_tok x n_heads] or NULL

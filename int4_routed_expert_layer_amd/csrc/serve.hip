@@ -327,6 +327,8 @@ coli_status coli_latent_decode(coli_serve *S, const void *q_lat, int64_t ql_tok_
     a.cache = view(S, cache, page_stride, n_pages, block_table, table_stride, table_cols);
     a.mask = tree_mask;
     a.mask_words = mask_words;
+    a.n_tok = n_tok;
+    a.n_seq = S->plan_seq;
     a.n_heads = S->d.n_heads;
     a.scale = scale;
     a.out = static_cast<uint8_t *>(out);
