@@ -570,14 +570,20 @@ __global__ __launch_bounds__(256) void join_kernel(DecodeArgs a) {
 
 // The plan of a step, by one workgroup: each sequence's rows are cut into
 // 64-row units and its key tiles into runs of at most `per`, the run length
-// with the shortest estimated time: for one to four rounds over the CUs the
-// smallest run length that fits that many rounds, at (per + kItemCost) tiles per
-// round, and the joining of the pieces.  With more units than four rounds hold, only units longer than a
+// with the shortest estimated time.  One round over the CUs: the smallest run
+// length that gives no more items than CUs, and takes as long as that.  Two to
+// four rounds: the smallest that fits them; the sequences are then taken in the
+// order of their runs' lengths and every other round is laid out backwards, so
+// that the CUs' sums come close to their mean (16 ragged trees of 25 nodes:
+// 45 + 45 tiles at most in the order of arrival, 71 so, at a mean of 64; 173 -> 154 us).
+// Each item costs kItemCost tiles more, and joining the pieces a tile per
+// kJoinItems.  With more units than four rounds hold, only units longer than a
 // CU's fair share are cut.
 constexpr int kPlanThreads = 1024;
 constexpr int kItemCost = 3;    // tiles: the queries, the first tile's latency and the partial result
 constexpr int kJoinItems = 64;  // pieces whose joining costs as much as a tile
 constexpr int kMinRun = 2;
+constexpr int kSortMost = 1024; // sequences that are put in order
 
 __device__ __forceinline__ int cut(int tiles, int per) { return max(1, (tiles + per - 1) / per); }
 
@@ -586,7 +592,7 @@ __global__ __launch_bounds__(kPlanThreads) void decode_plan_kernel(DecodePlan p,
                                                                    int32_t *err) {
     __shared__ int s_tmp[kPlanThreads / 64 + 1];
     __shared__ unsigned long long s_units, s_work;
-    __shared__ int s_most, s_count[kPlanThreads / 64];
+    __shared__ int s_most, s_count[kPlanThreads / 64], s_key[kSortMost], s_order[kSortMost];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     int4 *seq = reinterpret_cast<int4 *>(p.seq);         // units, tiles, first item, first slot
     if (tid == 0) {
@@ -641,7 +647,8 @@ __global__ __launch_bounds__(kPlanThreads) void decode_plan_kernel(DecodePlan p,
             hi = top;
         }
         const long long items = static_cast<long long>(items_at(hi));
-        const long long cost = static_cast<long long>(r) * (hi + kItemCost) * kJoinItems + (items > static_cast<long long>(units) ? items : 0);
+        const long long each = r == 1 ? hi : max(static_cast<long long>(hi), static_cast<long long>(s_work / n_cu) + hi / 8);
+        const long long cost = (each + static_cast<long long>(r) * kItemCost) * kJoinItems + (items > static_cast<long long>(units) ? items : 0);
         if (best == 0 || cost < best_cost) {
             best = hi;
             best_cost = cost;
@@ -650,10 +657,28 @@ __global__ __launch_bounds__(kPlanThreads) void decode_plan_kernel(DecodePlan p,
     if (best == 0) best = static_cast<int>((s_work + n_cu - 1) / n_cu);
     if (best < 1) best = 1;
 
+    // With more than one round, the sequences by falling length of their runs.
+    const bool sorted = n_seq <= kSortMost && items_at(best) > static_cast<unsigned long long>(n_cu);
+    __syncthreads();
+    if (sorted) {
+        int mine = 0;
+        if (tid < n_seq) {
+            const int split = cut(seq[tid].y, best);
+            mine = (seq[tid].y + split - 1) / split;
+            s_key[tid] = mine;
+        }
+        __syncthreads();
+        if (tid < n_seq) {
+            int rank = 0;
+            for (int b = 0; b < n_seq; ++b) rank += s_key[b] > mine || (s_key[b] == mine && b < tid);
+            s_order[rank] = tid;
+        }
+    }
     int n_items = 0, n_slots = 0, n_joins = 0;
     if (tid == 0) s_most = 1;
+    __syncthreads();
     for (int b0 = 0; b0 < n_seq; b0 += kPlanThreads) {
-        const int b = b0 + tid;
+        const int b = b0 + tid >= n_seq ? n_seq : sorted ? s_order[b0 + tid] : b0 + tid;
         int4 s = b < n_seq ? seq[b] : int4{0, 0, 0, 0};
         const int split = cut(s.y, best), count = s.x * split;
         int total;
@@ -677,21 +702,22 @@ __global__ __launch_bounds__(kPlanThreads) void decode_plan_kernel(DecodePlan p,
     }
     // Round r, place x: workgroup x runs on XCD x % 8, and neighbouring items
     // share keys, so a round's items lie in eight contiguous runs, one per XCD.
+    // Of more rounds than one, every other is laid out backwards.
     const int rounds = max(1, (n_items + n_cu - 1) / n_cu);
     const bool fits = rounds * n_cu <= p.item_cap && n_slots <= p.slot_cap && n_joins <= p.join_cap;
+    const int run = rounds > 1 ? n_cu / 8 : (n_items + 7) / 8;
     auto place = [&](int i) {
-        const int r = i / n_cu, at = i - r * n_cu, here = min(n_cu, n_items - r * n_cu), run = (here + 7) / 8;
+        const int r = i / n_cu, at = (r & 1) ? n_cu - 1 - (i - r * n_cu) : i - r * n_cu;
         return r * n_cu + (at % run) * 8 + at / run;
     };
     __syncthreads();
-    {
-        for (int i = tid; i < (fits ? rounds : 1) * n_cu; i += kPlanThreads) {
-            const int r = i / n_cu, x = i - r * n_cu, here = fits ? min(n_cu, n_items - r * n_cu) : 0, run = (here + 7) / 8;
-            if ((x >> 3) >= run || (x & 7) * run + (x >> 3) >= here) {
-                DecodeItem none{};
-                none.seq = r + 1 < rounds && fits ? kItemMore : 0;
-                p.items[i] = none;
-            }
+    for (int i = tid; i < (fits ? rounds : 1) * n_cu; i += kPlanThreads) {
+        const int r = i / n_cu, x = i - r * n_cu, here = fits ? min(n_cu, n_items - r * n_cu) : 0;
+        const int pos = (x & 7) * run + (x >> 3), at = (r & 1) ? n_cu - 1 - pos : pos;
+        if ((x >> 3) >= run || at >= here) {
+            DecodeItem none{};
+            none.seq = r + 1 < rounds && fits ? kItemMore : 0;
+            p.items[i] = none;
         }
     }
     if (fits)
