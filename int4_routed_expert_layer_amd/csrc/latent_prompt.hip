@@ -82,19 +82,26 @@ __device__ __forceinline__ void attend(const PromptArgs &a, const Tile &tile, ui
     constexpr int kShare = WAVES / 4, kMost = (H::kBlocks + kShare - 1) / kShare;
     const int part = wave >> 2, mine = (H::kBlocks - part + kShare - 1) / kShare;
     const int cr = 8 * (wave & 3) + (lane >> 3), unit = ((lane & 7) ^ dev::tile_swz(cr)) << 4;
-    auto copy_step = [&](int t) {
+    struct Copy {
+        const uint8_t *kv, *pe;
+        uint32_t dst;
+    };
+    auto aim = [&](int t) {
         const uint32_t dst = kv_lds + (t % kSlots) * H::kStepBytes + (wave & 3) * 1024;
         t = min(t, tile.steps - 1);                       // past the end the last step is copied again
         const int64_t key = tile.k0 + min(t * kStepKeys + cr, tile.nk - 1);
-        const uint8_t *kv = a.kv + (key * a.kv_tok + tile.head * a.kv_head) * 2 + unit;
-        const uint8_t *pe = a.k_pe + key * a.pe_tok * 2 + unit;
+        return Copy{a.kv + (key * a.kv_tok + tile.head * a.kv_head) * 2 + unit, a.k_pe + key * a.pe_tok * 2 + unit, dst};
+    };
+    auto copy = [&](const Copy &x, int i) {
+        const int b = kShare * i + part;
+        if (b >= H::kBlocks) return;
+        const uint8_t *src = b < H::kNopeBlocks ? x.kv + b * 128 : b == H::kNopeBlocks ? x.pe : x.kv + (b - 1) * 128;
+        dev::copy16_to_lds_free(src, x.dst + b * kBlockBytes);
+    };
+    auto copy_step = [&](int t) {
+        const Copy x = aim(t);
 #pragma unroll
-        for (int i = 0; i < kMost; ++i) {
-            const int b = kShare * i + part;
-            if (b >= H::kBlocks) break;
-            const uint8_t *src = b < H::kNopeBlocks ? kv + b * 128 : b == H::kNopeBlocks ? pe : kv + (b - 1) * 128;
-            dev::copy16_to_lds(src, dst + b * kBlockBytes);
-        }
+        for (int i = 0; i < kMost; ++i) copy(x, i);
     };
 
 #pragma unroll
@@ -105,45 +112,27 @@ __device__ __forceinline__ void attend(const PromptArgs &a, const Tile &tile, ui
     l = 0.0f;
     float limit = -__builtin_inff(), offset = 0.0f;       // of a score that calls for a new maximum; of the exponent
     if (tile.steps == 0) return;
-    copy_step(0);
-    copy_step(1);
-    for (int t = 0; t < tile.steps; ++t) {
-        // Step t has landed when only the copies of step t + 1 are in flight.
-        if (mine == kMost)
-            asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kMost) : "memory");
-        else
-            asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kMost - 1) : "memory");
-        dev::lds_barrier();
-        copy_step(t + 2);
-        if (t * kStepKeys >= shut) continue;
-        const uint8_t *kv = s_kv + (t % kSlots) * H::kStepBytes;
-        auto key = [&](int k) { return *reinterpret_cast<const u32x4 *>(kv + (k >> 2) * kBlockBytes + dev::tile_unit(l31, 2 * (k & 3) + lh)); };
-        f32x16 s;
+    auto key_row = [&](int t, int k) {
+        return *reinterpret_cast<const u32x4 *>(s_kv + (t % kSlots) * H::kStepBytes + (k >> 2) * kBlockBytes + dev::tile_unit(l31, 2 * (k & 3) + lh));
+    };
+    f32x16 s;                                             // scores of step t
+    // What follows the scores of a step: the mask, and where a row exceeds its
+    // maximum by more than the slack, the new maximum.
+    auto largest = [](const f32x16 &x) {
+        float mx = x[0];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) s[i] = 0.0f;
-        u32x4 kf[kAhead];
-#pragma unroll
-        for (int k = 0; k < kAhead; ++k) kf[k] = key(k);
-#pragma unroll
-        for (int k = 0; k < H::kDepth; ++k) {
-            s = dev::mma<BF>(kf[k % kAhead], q[k], s);
-            if (k + kAhead < H::kDepth) kf[k % kAhead] = key(k + kAhead);
-        }
-        dev::pipeline<H::kDepth, 1, 1, kAhead>();
-        __builtin_amdgcn_sched_barrier(0);
-        const bool masked = (t + 1) * kStepKeys > open;
-        const int seen = seen_all - t * kStepKeys - 4 * lh;
-        if (masked) {
+        for (int i = 1; i < 16; ++i) mx = fmaxf(mx, x[i]);
+        return mx;
+    };
+    auto settle = [&](int t, float mx) {
+        if ((t + 1) * kStepKeys > open) {
+            const int seen = seen_all - t * kStepKeys - 4 * lh;
 #pragma unroll
             for (int i = 0; i < 16; ++i)
                 if (8 * (i >> 2) + (i & 3) >= seen) s[i] = -__builtin_inff();
+            mx = largest(s);
         }
-        float mx = s[0];
-#pragma unroll
-        for (int i = 1; i < 16; ++i) mx = fmaxf(mx, s[i]);
         if (__any(mx > limit)) {
-            // The maximum of a row moves only when a step exceeds it by more
-            // than the slack.
             const float tm = dev::max_halves(mx) * c;
             const float m1 = tm > m + (m == -__builtin_inff() ? 0.0f : kSlack) ? tm : m;
             const float fac = m1 == m ? 1.0f : __builtin_amdgcn_exp2f(m - m1);
@@ -156,16 +145,65 @@ __device__ __forceinline__ void attend(const PromptArgs &a, const Tile &tile, ui
 #pragma unroll
                 for (int i = 0; i < 16; ++i) acc[cb][i] *= fac;
         }
-        u32x4 p[2];                                       // B operands of the two 16-key products
+    };
+    copy_step(0);
+    copy_step(1);
+    if (mine == kMost)
+        asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kMost) : "memory");
+    else
+        asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kMost - 1) : "memory");
+    dev::lds_barrier();
+    {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float e0 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[2 * j], c, offset));
-            const float e1 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[2 * j + 1], c, offset));
-            l += e0 + e1;
-            p[j >> 2][j & 3] = dev::pack2<BF>(e0, e1);
+        for (int i = 0; i < 16; ++i) s[i] = 0.0f;
+#pragma unroll
+        for (int k = 0; k < H::kDepth; ++k) s = dev::mma<BF>(key_row(0, k), q[k], s);
+        settle(0, largest(s));
+    }
+    Copy now = aim(2);
+    for (int t = 0; t < tile.steps; ++t) {
+        // Step t + 1 has landed, and step t - 1 is read no more.
+        dev::copy_barrier();
+        if (t * kStepKeys >= shut) {
+            copy_step(t + 2);
+            continue;
+        }
+        // The scores of step t + 1 (past the end, of the last step again) are
+        // formed while those of step t are weighed and step t + 2 is copied: in
+        // four parts of a quarter of each, because the wave stalls at a copy
+        // until the CU's address unit takes it (five in a row cost 670 of the
+        // step's 2420 clocks) and the products run on meanwhile.
+        f32x16 next;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) next[i] = 0.0f;
+        u32x4 kf[kAhead];
+        u32x4 p[2];                                       // B operands of the two 16-key products
+        constexpr int kPart = H::kDepth / 4;
+        now = aim(t + 2);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) kf[k] = key_row(t + 1, k);
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+#pragma unroll
+            for (int k = h * kPart; k < (h + 1) * kPart; ++k) {
+                next = dev::mma<BF>(kf[k % kAhead], q[k], next);
+                if (k + kAhead < H::kDepth) kf[k % kAhead] = key_row(t + 1, k + kAhead);
+            }
+#pragma unroll
+            for (int j = 2 * h; j < 2 * h + 2; ++j) {
+                const float e0 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[2 * j], c, offset));
+                const float e1 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[2 * j + 1], c, offset));
+                l += e0 + e1;
+                p[j >> 2][j & 3] = dev::pack2<BF>(e0, e1);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int i = h * kMost / 4; i < (h + 1) * kMost / 4; ++i) copy(now, i);
+            __builtin_amdgcn_sched_barrier(0);
         }
         // O^T: product k takes keys 16 k + 4 lh + 0..3 and 16 k + 8 + 4 lh + 0..3.
-        const uint8_t *vt = kv + H::kKeyBlocks * kBlockBytes + 8 * (lane & 1);
+        const uint8_t *vt = s_kv + (t % kSlots) * H::kStepBytes + H::kKeyBlocks * kBlockBytes + 8 * (lane & 1);
         const int vr = 4 * lh + ((lane >> 2) & 3);
         auto value = [&](int n) {                         // of product n: 16 keys n / (V / 32), columns 32 (n % (V / 32))
             const int k = n / (V / 32), cb = n % (V / 32);
@@ -175,7 +213,8 @@ __device__ __forceinline__ void attend(const PromptArgs &a, const Tile &tile, ui
             const u32x2 a1 = dev::read_tr(blk + dev::tile_unit(vr + 8, unit));
             return u32x4{a0[0], a0[1], a1[0], a1[1]};
         };
-        if (CAREFUL && masked) {
+        if (CAREFUL && (t + 1) * kStepKeys > open) {
+            const int seen = seen_all - t * kStepKeys - 4 * lh;
             const uint32_t one = BF ? 0x3F80u : 0x3C00u;
 #pragma unroll
             for (int cb = 0; cb < V / 32; ++cb) {
@@ -201,7 +240,6 @@ __device__ __forceinline__ void attend(const PromptArgs &a, const Tile &tile, ui
                     if (n[i] > 0.0f) acc[cb][i] = __builtin_nanf("");
             }
         } else {
-            __builtin_amdgcn_sched_barrier(0);
             constexpr int kN = 2 * (V / 32);
             u32x4 vf[kAhead];
 #pragma unroll
@@ -214,6 +252,8 @@ __device__ __forceinline__ void attend(const PromptArgs &a, const Tile &tile, ui
             dev::pipeline<2 * kN, 1, 2, 2 * kAhead>();
             __builtin_amdgcn_sched_barrier(0);
         }
+        s = next;
+        settle(t + 1, largest(next));
     }
     // The copies past the end land before the ring is used again.
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
