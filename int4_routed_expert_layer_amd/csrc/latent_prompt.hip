@@ -20,10 +20,19 @@ namespace coli {
 namespace {
 
 using dev::f32x16;
+using dev::f32x2;
+using dev::f32x4;
 using dev::u32x2;
 using dev::u32x4;
 
+constexpr int kRows = 128;        // query rows of a tile
 constexpr int kStepKeys = 32;
+// A call with few tiles divides the keys of each into parts: at least four steps
+// each (with sixteen, 64 rows of 1024 keys and 8 heads take 21 us instead of
+// 14.5; undivided they take 29) and at most 64 parts (20 rows of 60000 keys, one
+// head: 64 parts 58 us, 32 65 us, 128 75 us: the join reads them one after the other).
+constexpr int kLeastSteps = 4;
+constexpr int64_t kMostParts = 64;
 constexpr int kBlockBytes = kStepKeys * 128;
 constexpr int kRing = 4;          // of the wide head, whose values are read a step later
 constexpr float kSlack = 8.0f;    // see latent_decode.hip
@@ -46,6 +55,7 @@ struct Tile {
     int head, row0, rows;      // rows row0 .. row0 + rows - 1 of the sequence's queries
     int ahead;                 // row i sees keys up to i + ahead (causal)
     int steps;
+    int pieces, slot;          // parts the tile's keys are divided into; this one's place in the scratch
 };
 
 // The keys a row of the tile sees (the first `seen` ones).
@@ -58,7 +68,7 @@ __device__ __forceinline__ int seen_by(const PromptArgs &a, const Tile &t, int r
 // that are not finite are taken as zero where a step hides keys, and a second
 // product counts, per output, those that the row does see, which make that
 // output NaN.
-template <bool BF, int NOPE, int V, int WAVES, bool CAREFUL>
+template <bool BF, int NOPE, int V, bool CAREFUL>
 __device__ __forceinline__ void attend(const PromptArgs &a, const Tile &tile, uint8_t *s_kv, uint32_t kv_lds, f32x16 (&acc)[V / 32],
                                        float &m, float &l) {
     using H = Head<NOPE, V>;
@@ -77,31 +87,26 @@ __device__ __forceinline__ void attend(const PromptArgs &a, const Tile &tile, ui
         for (int k = 0; k < H::kDepth; ++k) q[k] = dev::gload<u32x4>(src + 32 * k);
     }
 
-    // Copies: wave w takes keys 8 (w % 4) .. + 7 of a step, a 16-byte unit per
-    // lane of every block, or with eight waves of every other block.
-    constexpr int kShare = WAVES / 4, kMost = (H::kBlocks + kShare - 1) / kShare;
-    const int part = wave >> 2, mine = (H::kBlocks - part + kShare - 1) / kShare;
-    const int cr = 8 * (wave & 3) + (lane >> 3), unit = ((lane & 7) ^ dev::tile_swz(cr)) << 4;
+    // Copies: keys 8 w .. + 7 of a step, a 16-byte unit of every block per lane.
+    const int cr = 8 * wave + (lane >> 3), unit = ((lane & 7) ^ dev::tile_swz(cr)) << 4;
     struct Copy {
         const uint8_t *kv, *pe;
         uint32_t dst;
     };
     auto aim = [&](int t) {
-        const uint32_t dst = kv_lds + (t % kSlots) * H::kStepBytes + (wave & 3) * 1024;
+        const uint32_t dst = kv_lds + (t % kSlots) * H::kStepBytes + wave * 1024;
         t = min(t, tile.steps - 1);                       // past the end the last step is copied again
         const int64_t key = tile.k0 + min(t * kStepKeys + cr, tile.nk - 1);
         return Copy{a.kv + (key * a.kv_tok + tile.head * a.kv_head) * 2 + unit, a.k_pe + key * a.pe_tok * 2 + unit, dst};
     };
-    auto copy = [&](const Copy &x, int i) {
-        const int b = kShare * i + part;
-        if (b >= H::kBlocks) return;
+    auto copy = [&](const Copy &x, int b) {
         const uint8_t *src = b < H::kNopeBlocks ? x.kv + b * 128 : b == H::kNopeBlocks ? x.pe : x.kv + (b - 1) * 128;
         dev::copy16_to_lds_free(src, x.dst + b * kBlockBytes);
     };
     auto copy_step = [&](int t) {
         const Copy x = aim(t);
 #pragma unroll
-        for (int i = 0; i < kMost; ++i) copy(x, i);
+        for (int b = 0; b < H::kBlocks; ++b) copy(x, b);
     };
 
 #pragma unroll
@@ -148,10 +153,7 @@ __device__ __forceinline__ void attend(const PromptArgs &a, const Tile &tile, ui
     };
     copy_step(0);
     copy_step(1);
-    if (mine == kMost)
-        asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kMost) : "memory");
-    else
-        asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kMost - 1) : "memory");
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(H::kBlocks) : "memory");
     dev::lds_barrier();
     {
 #pragma unroll
@@ -160,7 +162,6 @@ __device__ __forceinline__ void attend(const PromptArgs &a, const Tile &tile, ui
         for (int k = 0; k < H::kDepth; ++k) s = dev::mma<BF>(key_row(0, k), q[k], s);
         settle(0, largest(s));
     }
-    Copy now = aim(2);
     for (int t = 0; t < tile.steps; ++t) {
         // Step t + 1 has landed, and step t - 1 is read no more.
         dev::copy_barrier();
@@ -179,7 +180,7 @@ __device__ __forceinline__ void attend(const PromptArgs &a, const Tile &tile, ui
         u32x4 kf[kAhead];
         u32x4 p[2];                                       // B operands of the two 16-key products
         constexpr int kPart = H::kDepth / 4;
-        now = aim(t + 2);
+        const Copy now = aim(t + 2);
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) kf[k] = key_row(t + 1, k);
@@ -199,7 +200,7 @@ __device__ __forceinline__ void attend(const PromptArgs &a, const Tile &tile, ui
             }
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int i = h * kMost / 4; i < (h + 1) * kMost / 4; ++i) copy(now, i);
+            for (int b = h * H::kBlocks / 4; b < (h + 1) * H::kBlocks / 4; ++b) copy(now, b);
             __builtin_amdgcn_sched_barrier(0);
         }
         // O^T: product k takes keys 16 k + 4 lh + 0..3 and 16 k + 8 + 4 lh + 0..3.
@@ -259,16 +260,22 @@ __device__ __forceinline__ void attend(const PromptArgs &a, const Tile &tile, ui
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 }
 
-// The row tile (of ROWS rows) of this workgroup; false where it has none.
-// Workgroups of one XCD (blockIdx % 8) take the row tiles of the same heads,
-// which share K and V in its L2; the last tiles, which see the most keys,
-// come first.
-template <int ROWS>
-__device__ __forceinline__ bool find_tile(const PromptArgs &a, int tiles_cap, Tile &tile) {
+// The place of this workgroup among `total`: those of one XCD (blockIdx % 8)
+// follow each other.  Negative where it has none.
+__device__ __forceinline__ int place_of(int total) {
+    const int share = (total + 7) / 8, xcd = blockIdx.x & 7, i = blockIdx.x >> 3;
+    return i < share && xcd * share + i < total ? xcd * share + i : -1;
+}
+
+// The row tile of place `slot`, or the part of its keys that the place takes
+// where a call has few tiles; false where it has none.  The row tiles of one
+// head, which share K and V in an XCD's L2, follow each other; the last tiles,
+// which see the most keys, come first.
+__device__ __forceinline__ bool find_tile(const PromptArgs &a, int tiles_cap, int slot, Tile &tile) {
     const int lane = threadIdx.x & 63;
-    const int total = a.n_heads * tiles_cap, share = (total + 7) / 8;
-    const int lin = static_cast<int>(blockIdx.x & 7) * share + static_cast<int>(blockIdx.x >> 3);
-    if (static_cast<int>(blockIdx.x >> 3) >= share || lin >= total) return false;
+    if (slot < 0) return false;
+    tile.slot = slot;
+    const int lin = slot / a.split, piece = slot - lin * a.split;
     tile.head = lin / tiles_cap;
     const int want = tiles_cap - 1 - (lin - tile.head * tiles_cap);
     // Sequence and row tile number `want` of the call: each lane counts one
@@ -283,7 +290,7 @@ __device__ __forceinline__ bool find_tile(const PromptArgs &a, int tiles_cap, Ti
             q1 = a.q_start[b + 1];
             k0 = a.k_start[b];
             k1 = a.k_start[b + 1];
-            if (q0 >= 0 && q1 >= q0 && q1 <= a.n_q) n = (q1 - q0 + ROWS - 1) / ROWS;
+            if (q0 >= 0 && q1 >= q0 && q1 <= a.n_q) n = (q1 - q0 + kRows - 1) / kRows;
             else bad_seq = true;
         }
         int cum = n;
@@ -311,28 +318,101 @@ __device__ __forceinline__ bool find_tile(const PromptArgs &a, int tiles_cap, Ti
         dev::flag_if(threadIdx.x == 0, a.err, kErrSeq);
         tile.k0 = tile.nk = 0;
     }
-    tile.row0 = number * ROWS;
-    tile.rows = min(ROWS, nq - tile.row0);
+    tile.row0 = number * kRows;
+    tile.rows = min(kRows, nq - tile.row0);
     tile.ahead = tile.nk - nq;
     const int last = seen_by(a, tile, tile.rows - 1);
     tile.steps = last > 0 ? (last + kStepKeys - 1) / kStepKeys : 0;
+    // A part is a tile whose sequence begins at the part's first key.
+    tile.pieces = min(a.split, max(1, tile.steps / kLeastSteps));
+    if (piece >= tile.pieces) return false;
+    const int t0 = piece * tile.steps / tile.pieces, t1 = (piece + 1) * tile.steps / tile.pieces;
+    tile.k0 += t0 * kStepKeys;
+    tile.nk -= t0 * kStepKeys;
+    tile.ahead -= t0 * kStepKeys;
+    tile.steps = t1 - t0;
     return true;
 }
 
-template <bool BF, int NOPE, int V, int WAVES>
-__global__ __launch_bounds__(64 * WAVES, 2) void latent_prompt_kernel(PromptArgs a, int tiles_cap) {
+// Partial outputs of a part: block b (32 columns of 32 rows) as its registers
+// hold it, four to a store, 256 threads.
+template <int V>
+__device__ __forceinline__ float *part_of(const PromptArgs &a, int slot, int block) {
+    return a.part + (static_cast<int64_t>(slot) * (V / 32) + block) * (16 * 256) + (threadIdx.x & 255) * 4;
+}
+template <int V>
+__device__ __forceinline__ void store_part(const PromptArgs &a, int slot, int block, const f32x16 &acc) {
+    float *at = part_of<V>(a, slot, block);
+#pragma unroll
+    for (int g = 0; g < 4; ++g) *reinterpret_cast<f32x4 *>(at + g * 1024) = f32x4{acc[4 * g], acc[4 * g + 1], acc[4 * g + 2], acc[4 * g + 3]};
+}
+
+// Tiles whose keys were divided: out = sum_i f_i O_i / sum_i f_i l_i with
+// f_i = 2^(m_i - max m).  A workgroup joins one block of a tile; its threads
+// stand where those that stored the parts stood.
+template <bool BF, int V, bool WIDE>
+__global__ __launch_bounds__(256) void join_parts_kernel(PromptArgs a, int tiles_cap) {
+    Tile tile;
+    const int place = place_of(a.n_heads * tiles_cap);
+    if (!find_tile(a, tiles_cap, place < 0 ? place : place * a.split, tile) || tile.pieces == 1) return;
+    const int wave = dev::wave_id(), l31 = threadIdx.x & 31, lh = (threadIdx.x & 63) >> 5, block = blockIdx.y;
+    const int row = WIDE ? 32 * (block & 3) + l31 : 32 * wave + l31;
+    const int col = WIDE ? wave * (V / 4) + 32 * (block >> 2) : 32 * block;
+    // Four parts' loads are in flight at a time.
+    constexpr int kBatch = 4;
+    const f32x2 *ml = reinterpret_cast<const f32x2 *>(a.part_ml) + static_cast<int64_t>(tile.slot) * kRows + row;
+    const int last = tile.pieces - 1;
+    float m = -__builtin_inff(), l = 0.0f;
+    for (int i = 0; i < tile.pieces; i += 2 * kBatch) {
+        float mi[2 * kBatch];
+#pragma unroll
+        for (int j = 0; j < 2 * kBatch; ++j) mi[j] = ml[min(i + j, last) * kRows][0];
+#pragma unroll
+        for (int j = 0; j < 2 * kBatch; ++j) m = fmaxf(m, mi[j]);
+    }
+    f32x16 acc;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) acc[i] = 0.0f;
+    for (int i = 0; i < tile.pieces; i += kBatch) {
+        f32x2 mli[kBatch];
+        f32x4 x[kBatch][4];
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            const int p = min(i + j, last);
+            const float *at = part_of<V>(a, tile.slot + p, block);
+            mli[j] = ml[p * kRows];
+#pragma unroll
+            for (int g = 0; g < 4; ++g) x[j][g] = *reinterpret_cast<const f32x4 *>(at + g * 1024);
+        }
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            if (i + j > last) break;
+            const float f = mli[j][0] == m ? 1.0f : __builtin_amdgcn_exp2f(mli[j][0] - m);
+            l = __builtin_fmaf(f, mli[j][1], l);
+#pragma unroll
+            for (int k = 0; k < 16; ++k) acc[k] = __builtin_fmaf(f, x[j][k >> 2][k & 3], acc[k]);
+        }
+    }
+    const int64_t out_row = static_cast<int64_t>(tile.q0 + tile.row0 + row) * a.n_heads + tile.head;
+    dev::store_tile16<BF>(acc, l == 0.0f ? 0.0f : 1.0f / l, row < tile.rows ? a.out + (out_row * V + col) * 2 : nullptr);
+    if (a.lse && block == (WIDE ? block & 3 : 0) && lh == 0 && (!WIDE || wave == 0) && row < tile.rows)
+        a.lse[out_row] = l == 0.0f ? -__builtin_inff() : (m + __builtin_amdgcn_logf(l)) * kLn2;
+}
+
+template <bool BF, int NOPE, int V>
+__global__ __launch_bounds__(256, 2) void latent_prompt_kernel(PromptArgs a, int tiles_cap) {
     __shared__ __align__(1024) uint8_t s_kv[kSlots * Head<NOPE, V>::kStepBytes];
     __shared__ int s_bad;
     const int tid = threadIdx.x, lane = tid & 63, wave = dev::wave_id();
     const int l31 = lane & 31, lh = lane >> 5;
     const uint32_t kv_lds = dev::lds_address(s_kv);
     Tile tile;
-    if (!find_tile<32 * WAVES>(a, tiles_cap, tile)) return;
+    if (!find_tile(a, tiles_cap, place_of(a.n_heads * tiles_cap * a.split), tile)) return;
 
     f32x16 acc[V / 32];                                   // [32 columns][32 rows] blocks of O^T
     float m, l;
     if (tid == 0) s_bad = 0;
-    attend<BF, NOPE, V, WAVES, false>(a, tile, s_kv, kv_lds, acc, m, l);
+    attend<BF, NOPE, V, false>(a, tile, s_kv, kv_lds, acc, m, l);
     // Anything that is not finite: again with care, if a step hides keys.
     float z = 0.0f;
 #pragma unroll
@@ -342,10 +422,16 @@ __global__ __launch_bounds__(64 * WAVES, 2) void latent_prompt_kernel(PromptArgs
     dev::lds_barrier();
     if (__any(z != 0.0f)) s_bad = 1;
     dev::lds_barrier();
-    if (s_bad) attend<BF, NOPE, V, WAVES, true>(a, tile, s_kv, kv_lds, acc, m, l);
+    if (s_bad) attend<BF, NOPE, V, true>(a, tile, s_kv, kv_lds, acc, m, l);
 
     const int row = 32 * wave + l31;
     l = dev::sum_halves(l);
+    if (tile.pieces > 1) {
+#pragma unroll
+        for (int cb = 0; cb < V / 32; ++cb) store_part<V>(a, tile.slot, cb, acc[cb]);
+        if (lh == 0) *reinterpret_cast<f32x2 *>(a.part_ml + (static_cast<int64_t>(tile.slot) * kRows + row) * 2) = f32x2{m, l};
+        return;
+    }
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
     const int64_t out_row = static_cast<int64_t>(tile.q0 + tile.row0 + row) * a.n_heads + tile.head;
     uint8_t *o = row < tile.rows ? a.out + out_row * V * 2 : nullptr;
@@ -365,7 +451,6 @@ __global__ __launch_bounds__(64 * WAVES, 2) void latent_prompt_kernel(PromptArgs
 // value columns each add step t - 1 for all rows and copy step t + 2.  Each
 // SIMD holds one of either kind.  A row's scores lie in one wave, which moves
 // its maximum by itself and leaves the rows' factors for the summing waves.
-constexpr int kSplitRows = 128;
 constexpr int kSplitThreads = 512;
 
 __device__ __forceinline__ int weight_unit(int r, int q) { return r * 64 + ((q ^ ((r >> 2) & 3)) << 4); }
@@ -399,7 +484,7 @@ __device__ __forceinline__ void score_rows(const PromptArgs &a, const Tile &tile
     for (int t = 0; t < tile.steps; ++t) {
         dev::lds_barrier();
         if (lane == 0) sh.raise[((t + 1) % 3) * 4 + wave] = 0;
-        uint8_t *pw = sh.p + (t & 1) * (kSplitRows * 64);
+        uint8_t *pw = sh.p + (t & 1) * (kRows * 64);
         if (t * kStepKeys >= shut) {
 #pragma unroll
             for (int g = 0; g < 4; ++g) *reinterpret_cast<u32x2 *>(pw + weight_unit(row, g) + 8 * lh) = u32x2{0, 0};
@@ -439,7 +524,7 @@ __device__ __forceinline__ void score_rows(const PromptArgs &a, const Tile &tile
             l *= fac;
             limit = m == -__builtin_inff() ? m : (m + kSlack) / c;
             offset = m == -__builtin_inff() ? 0.0f : -m;
-            if (lh == 0) sh.fac[(t & 1) * kSplitRows + row] = fac;
+            if (lh == 0) sh.fac[(t & 1) * kRows + row] = fac;
             if (lane == 0) sh.raise[(t % 3) * 4 + wave] = 1;
         }
 #pragma unroll
@@ -494,7 +579,7 @@ __device__ __forceinline__ bool sum_columns(const PromptArgs &a, const Tile &til
     const int vr = 8 * lh + ((lane >> 2) & 3);
     auto step = [&](int t, bool more, Copy &now) {
         const u32x4 raise = *reinterpret_cast<const u32x4 *>(sh.raise + (t % 3) * 4);
-        const uint8_t *pr = sh.p + (t & 1) * (kSplitRows * 64);
+        const uint8_t *pr = sh.p + (t & 1) * (kRows * 64);
         const uint8_t *vt = sh.kv + (t & (kRing - 1)) * H::kStepBytes + H::kKeyBlocks * kBlockBytes + 8 * (lane & 1);
         u32x4 pf[2][4], vf[2][kCols];
 #pragma unroll
@@ -515,7 +600,7 @@ __device__ __forceinline__ bool sum_columns(const PromptArgs &a, const Tile &til
 #pragma unroll
         for (int rb = 0; rb < 4; ++rb)
             if (__builtin_amdgcn_readfirstlane(raise[rb])) {
-                const float f = sh.fac[(t & 1) * kSplitRows + 32 * rb + l31];
+                const float f = sh.fac[(t & 1) * kRows + 32 * rb + l31];
 #pragma unroll
                 for (int cb = 0; cb < kCols; ++cb)
 #pragma unroll
@@ -601,15 +686,15 @@ __device__ __forceinline__ bool sum_columns(const PromptArgs &a, const Tile &til
 template <bool BF, int NOPE, int V>
 __global__ __launch_bounds__(kSplitThreads, 2) void latent_prompt_split_kernel(PromptArgs a, int tiles_cap) {
     __shared__ __align__(1024) uint8_t s_kv[kRing * Head<NOPE, V>::kStepBytes];
-    __shared__ __align__(1024) uint8_t s_p[2 * kSplitRows * 64];
-    __shared__ float s_fac[2 * kSplitRows], s_sum[kSplitRows];
+    __shared__ __align__(1024) uint8_t s_p[2 * kRows * 64];
+    __shared__ float s_fac[2 * kRows], s_sum[kRows];
     __shared__ __align__(16) int s_raise[12];
     __shared__ int s_bad;
     const int tid = threadIdx.x, lane = tid & 63, wave = dev::wave_id();
     const int l31 = lane & 31;
     const uint32_t kv_lds = dev::lds_address(s_kv);
     Tile tile;
-    if (!find_tile<kSplitRows>(a, tiles_cap, tile)) return;
+    if (!find_tile(a, tiles_cap, place_of(a.n_heads * tiles_cap * a.split), tile)) return;
     const Shared sh{s_kv, s_p, s_fac, s_sum, s_raise};
     const int64_t first = static_cast<int64_t>(tile.q0 + tile.row0) * a.n_heads + tile.head;
     if (tid == 0) s_bad = 0;
@@ -626,6 +711,10 @@ __global__ __launch_bounds__(kSplitThreads, 2) void latent_prompt_split_kernel(P
         }
         const int row = 32 * wave + l31;
         const float l = s_sum[row];
+        if (tile.pieces > 1) {
+            if (lane < 32) *reinterpret_cast<f32x2 *>(a.part_ml + (static_cast<int64_t>(tile.slot) * kRows + row) * 2) = f32x2{m, l};
+            return;
+        }
         if (a.lse && lane < 32 && row < tile.rows)
             a.lse[first + static_cast<int64_t>(row) * a.n_heads] = l == 0.0f ? -__builtin_inff() : (m + __builtin_amdgcn_logf(l)) * kLn2;
     } else {
@@ -637,6 +726,13 @@ __global__ __launch_bounds__(kSplitThreads, 2) void latent_prompt_split_kernel(P
             dev::lds_barrier();
             sum_columns<BF, NOPE, V, true>(a, tile, sh, kv_lds, acc);
             dev::lds_barrier();
+        }
+        if (tile.pieces > 1) {
+#pragma unroll
+            for (int cb = 0; cb < V / 128; ++cb)
+#pragma unroll
+                for (int rb = 0; rb < 4; ++rb) store_part<V>(a, tile.slot, 4 * cb + rb, acc[cb][rb]);
+            return;
         }
 #pragma unroll
         for (int rb = 0; rb < 4; ++rb) {
@@ -650,26 +746,33 @@ __global__ __launch_bounds__(kSplitThreads, 2) void latent_prompt_split_kernel(P
 }
 
 // Row tiles of a call, an upper bound (every sequence may end in a part of
-// one), and the workgroups for them, a multiple of the XCDs.
-template <typename K>
-hipError_t launch_tiles(const PromptArgs &a, K kernel, int rows, int threads, hipStream_t s) {
-    const int64_t cap = std::min<int64_t>(a.n_q, a.n_q / rows + a.n_seq);
-    const int64_t grid = (cap * a.n_heads + 7) / 8 * 8;
+// one), and the workgroups for them, a multiple of the XCDs.  A call with fewer
+// tiles than the chip holds workgroups divides the keys of each.
+template <typename K, typename J>
+hipError_t launch_tiles(PromptArgs &a, K kernel, J join, int threads, int blocks, int places, hipStream_t s) {
+    const int64_t seqs = std::min(a.n_seq, a.n_q), cap = (a.n_q - seqs) / kRows + seqs, tiles = cap * a.n_heads;
+    const int64_t most = (a.n_k + kStepKeys - 1) / kStepKeys / kLeastSteps;
+    a.split = static_cast<int>(std::max<int64_t>(1, std::min({std::min(places, a.part_cap) / tiles, most, kMostParts})));
+    const int64_t grid = (tiles * a.split + 7) / 8 * 8;
     if (grid > INT32_MAX) return hipErrorInvalidValue;
     launch(kernel, static_cast<unsigned>(grid), threads, 0, s, a, static_cast<int>(cap));
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess || a.split == 1) return e;
+    launch(join, dim3(static_cast<unsigned>((tiles + 7) / 8 * 8), blocks), 256, 0, s, a, static_cast<int>(cap));
     return hipGetLastError();
 }
 
 template <bool BF>
-hipError_t launch_typed(const PromptArgs &a, int nope, hipStream_t s) {
-    if (nope == 192) return launch_tiles(a, latent_prompt_split_kernel<BF, 192, 256>, kSplitRows, kSplitThreads, s);
-    return launch_tiles(a, latent_prompt_kernel<BF, 128, 128, 4>, 128, 256, s);
+hipError_t launch_typed(PromptArgs &a, int nope, int n_cu, hipStream_t s) {
+    if (nope == 192)
+        return launch_tiles(a, latent_prompt_split_kernel<BF, 192, 256>, join_parts_kernel<BF, 256, true>, kSplitThreads, 256 / 32, n_cu, s);
+    return launch_tiles(a, latent_prompt_kernel<BF, 128, 128>, join_parts_kernel<BF, 128, false>, 256, 128 / 32, 2 * n_cu, s);
 }
 
 }  // namespace
 
-hipError_t launch_latent_prompt(const PromptArgs &a, bool bf16, int nope, hipStream_t s) {
-    return bf16 ? launch_typed<true>(a, nope, s) : launch_typed<false>(a, nope, s);
+hipError_t launch_latent_prompt(PromptArgs a, bool bf16, int nope, int n_cu, hipStream_t s) {
+    return bf16 ? launch_typed<true>(a, nope, n_cu, s) : launch_typed<false>(a, nope, n_cu, s);
 }
 
 }  // namespace coli

@@ -76,6 +76,9 @@ struct PromptArgs {
     float scale;
     uint8_t *out;              // [n_q x n_heads x v]
     float *lse;                // [n_q x n_heads] or NULL
+    float *part;               // [part_cap x 128 x v], in the order of join_parts_kernel's blocks
+    float *part_ml;            // [part_cap x 128 x 2]
+    int part_cap, split;       // split: set by the launcher, parts per tile at most
     int32_t *err;
 };
 
@@ -128,7 +131,7 @@ hipError_t launch_keep(const KeepArgs &a, hipStream_t s);
 hipError_t launch_decode_plan(const DecodePlan &p, const int32_t *q_start, const int32_t *kv_len, int n_seq, int n_tok,
                               int n_heads, int n_cu, int32_t *err, hipStream_t s);
 hipError_t launch_latent_decode(const DecodeArgs &a, bool bf16, int n_cu, hipStream_t s);
-hipError_t launch_latent_prompt(const PromptArgs &a, bool bf16, int nope, hipStream_t s);
+hipError_t launch_latent_prompt(PromptArgs a, bool bf16, int nope, int n_cu, hipStream_t s);
 hipError_t launch_verify(const VerifyArgs &a, int n_cu, hipStream_t s);
 
 // abi.hip: device memory under the library's allocation book and cap.

@@ -374,9 +374,12 @@ coli_status coli_latent_prompt(coli_serve *S, const void *q, int64_t q_tok_strid
     a.scale = scale;
     a.out = static_cast<uint8_t *>(out);
     a.lse = lse;
+    a.part = S->part;
+    a.part_ml = S->part_ml;
+    a.part_cap = S->plan.slot_cap / 2;   // two 64 x 512 slots hold a part of 128 rows and up to 256 columns, with its statistics
     a.err = S->err;
     OnDevice on(S->device);
-    return launched(S, launch_latent_prompt(a, S->d.half == COLI_HALF_BF16, S->d.nope, static_cast<hipStream_t>(stream)), "prompt launch");
+    return launched(S, launch_latent_prompt(a, S->d.half == COLI_HALF_BF16, S->d.nope, S->n_cu, static_cast<hipStream_t>(stream)), "prompt launch");
 }
 
 coli_status coli_draft_verify(coli_serve *S, const void *probs, int64_t probs_stride, const void *draft, int64_t draft_stride, int32_t kind,

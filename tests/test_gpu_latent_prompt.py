@@ -121,6 +121,35 @@ def test_a_long_prompt_and_the_same_bits_twice(width):
 
 
 @pytest.mark.parametrize("width", ["wide", "narrow"])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("n,nk", [([40], [2501]), ([1, 300, 5], [1800, 2100, 4]), ([900], [900]), ([1000], [700])])
+def test_few_rows_of_many_keys(width, dtype, causal, n, nk):
+    """Calls with few tiles, whose keys are divided: parts that some rows or all see, and sequences too short for parts."""
+    c = Case(n, nk, 2, width, dtype, causal=causal, seed=11)
+    out, lse = c.run()
+    c.check(out, lse)
+    again, again_lse = c.run()
+    assert torch.equal(out, again) and torch.equal(lse, again_lse)
+
+
+@pytest.mark.parametrize("width", ["wide", "narrow"])
+def test_values_that_are_not_finite_in_divided_keys(width):
+    """Key 1600 of 1650 is hidden from the first 30 of 80 queries and its value is inf in one column."""
+    c = Case([80], [1650], 2, width, seed=12)
+    clean, clean_lse = c.run()
+    c.kv[1600, 1, c.nope + 9] = float("inf")
+    out, lse = c.run()
+    assert torch.equal(out[:30], clean[:30]) and torch.equal(out[:, 0], clean[:, 0]) and torch.equal(lse, clean_lse)
+    assert not torch.isfinite(out[30:, 1, 9]).any()
+    assert torch.equal(out[:, 1, :9], clean[:, 1, :9]) and torch.equal(out[:, 1, 10:], clean[:, 1, 10:])
+    c.kv[1600, 1, c.nope + 9] = 0.5
+    c.kv[100, 1, 3] = float("nan")                          # a key that all see
+    out, lse = c.run()
+    assert torch.isnan(out[:, 1]).all() and torch.isnan(lse[:, 1]).all() and torch.equal(lse[:, 0], clean_lse[:, 0])
+
+
+@pytest.mark.parametrize("width", ["wide", "narrow"])
 def test_many_sequences_and_uncovered_tokens(width):
     n = [int(x) for x in np.random.default_rng(6).integers(0, 40, 150)]
     c = Case(n, n, 1, width, seed=6)
