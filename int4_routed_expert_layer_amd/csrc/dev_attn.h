@@ -80,6 +80,18 @@ __device__ __forceinline__ uint32_t nonfinite_halves(uint32_t w) {
 __device__ __forceinline__ int tile_swz(int r) { return (r >> 1) & 7; }
 __device__ __forceinline__ int tile_unit(int r, int q) { return r * 128 + ((q ^ tile_swz(r)) << 4); }
 
+// Sum of the lanes up to this one, in the registers (shuffles by way of LDS take
+// six latencies of it).
+__device__ __forceinline__ int running_sum(int v) {
+    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false);   // row_shr:1 .. 8 within 16 lanes
+    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);   // row_bcast:15 into rows 1 and 3
+    v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);   // row_bcast:31 into rows 2 and 3
+    return v;
+}
+
 // Transposed read: each 16-lane group reads a 4 x 16 block (lane i gives the
 // address of row i / 4, columns 4 (i % 4) .. + 3) and lane i gets column i of
 // its four rows.
@@ -172,24 +184,56 @@ __device__ __forceinline__ void pipeline() {
     pipeline_run<READS_ALL - AHEAD, MFMAS, READS>();
 }
 
-// Stores 32 columns x 32 rows of an accumulator as 16-bit values: lane L holds
-// row L % 32 and columns 8 g + 4 (L / 32) + 0..3 in registers 4 g .. 4 g + 3;
-// the lanes of a row trade halves so that each stores 16 bytes.  `row` is the
-// lane's row at the tile's first column, NULL for a row that is not stored.
+// Sixteen bytes of a 32 x 32 accumulator as 16-bit values: lane L holds row L %
+// 32 and columns 8 g + 4 (L / 32) + 0..3 in registers 4 g .. 4 g + 3; the lanes
+// of a row trade halves, and L gets columns 8 (G + L / 32) .. + 7.
+template <bool BF, int G>
+__device__ __forceinline__ u32x4 pack_tile16(const f32x16 &acc, float by) {
+    uint32_t w[2][2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int d = 0; d < 2; ++d)
+            w[k][d] = pack2<BF>(acc[4 * (G + k) + 2 * d] * by, acc[4 * (G + k) + 2 * d + 1] * by);
+    const auto a = __builtin_amdgcn_permlane32_swap(w[0][0], w[1][0], false, false);
+    const auto b = __builtin_amdgcn_permlane32_swap(w[0][1], w[1][1], false, false);
+    return u32x4{a[0], b[0], a[1], b[1]};
+}
+// Stores 32 columns x 32 rows.  `row` is the lane's row at the tile's first
+// column, NULL for a row that is not stored.
 template <bool BF>
 __device__ __forceinline__ void store_tile16(const f32x16 &acc, float by, uint8_t *row) {
     const int lh = (threadIdx.x & 63) >> 5;
+    const u32x4 x = pack_tile16<BF, 0>(acc, by), y = pack_tile16<BF, 2>(acc, by);
+    if (!row) return;
+    *reinterpret_cast<u32x4 *>(row + 16 * lh) = x;
+    *reinterpret_cast<u32x4 *>(row + 16 * (2 + lh)) = y;
+}
+// Stores 64 columns x 32 rows by way of 4 KB of LDS that the wave has to itself,
+// 128 bytes of a row together (as 32 bytes of 32 rows each store occupies the
+// CU's address unit longer: 32 prompts of 128 rows, 64 heads, 256 columns 167 us,
+// so 137; 128 columns 76 and 71).  `by` is of the lane's row L % 32, `at` row 0,
+// `rows` the rows stored, `stride` their distance in bytes.
+template <bool BF>
+__device__ __forceinline__ void store_rows16(const f32x16 &acc0, const f32x16 &acc1, float by, uint8_t *lds, uint8_t *at, int64_t stride, int rows) {
+    int lane = threadIdx.x & 63;
+    // What the area held before has been read.  Nor does the compiler see that
+    // the lane's addresses here are like those of a caller's loop: it would hold
+    // their parts in registers across it (500 spilled ones in the narrow head).
+    asm volatile("" : "+v"(lane)::"memory");
+    const int l31 = lane & 31, lh = lane >> 5;
+    *reinterpret_cast<u32x4 *>(lds + tile_unit(l31, lh)) = pack_tile16<BF, 0>(acc0, by);
+    *reinterpret_cast<u32x4 *>(lds + tile_unit(l31, 2 + lh)) = pack_tile16<BF, 2>(acc0, by);
+    *reinterpret_cast<u32x4 *>(lds + tile_unit(l31, 4 + lh)) = pack_tile16<BF, 0>(acc1, by);
+    *reinterpret_cast<u32x4 *>(lds + tile_unit(l31, 6 + lh)) = pack_tile16<BF, 2>(acc1, by);
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    u32x4 v[4];
 #pragma unroll
-    for (int g = 0; g < 4; g += 2) {
-        uint32_t w[2][2];
+    for (int j = 0; j < 4; ++j) v[j] = *reinterpret_cast<const u32x4 *>(lds + tile_unit(8 * j + (lane >> 3), lane & 7));
 #pragma unroll
-        for (int k = 0; k < 2; ++k)
-#pragma unroll
-            for (int d = 0; d < 2; ++d)
-                w[k][d] = pack2<BF>(acc[4 * (g + k) + 2 * d] * by, acc[4 * (g + k) + 2 * d + 1] * by);
-        const auto a = __builtin_amdgcn_permlane32_swap(w[0][0], w[1][0], false, false);
-        const auto b = __builtin_amdgcn_permlane32_swap(w[0][1], w[1][1], false, false);
-        if (row) *reinterpret_cast<u32x4 *>(row + 16 * (g + lh)) = u32x4{a[0], b[0], a[1], b[1]};
+    for (int j = 0; j < 4; ++j) {
+        const int r = 8 * j + (lane >> 3);
+        if (r < rows) *reinterpret_cast<u32x4 *>(at + r * stride + 16 * (lane & 7)) = v[j];
     }
 }
 

@@ -27,12 +27,13 @@
 // pieces leave unnormalised sums, maxima and fp32 partial outputs, which
 // join_kernel combines.
 //
-// Measured, 64 heads.  64 tokens of sequences up to 12k, bf16: 68 us and 9.2 for the
-// join, 352 MB, 5.2 TB/s in the first: bound by HBM.  Four chains of four tokens up to 128k, f16: 96
-// and 12, 535 MB, 5.6 TB/s.  16 trees of 25 nodes up to 4k, bf16: 153 us, 940 TFLOP/s
-// against 1223 of a large library product: bound by the matrix units and
-// their clock under load.  One token, 4k: 13.8 and 5.2 us, a chain of latencies (the
-// item, its queries, page numbers, keys, two steps, partial results).
+// Measured.  64 tokens of sequences up to 12k, 64 heads, bf16: 68 us and 9 for the
+// join, 352 MB, 5.2 TB/s in the first: bound by HBM.  Four chains of four tokens up
+// to 128k, 16 heads, f16: 96 and 12 us, 535 MB, 5.6 TB/s.  16 trees of 25 nodes up
+// to 5k, 64 heads, bf16: 153 us, 940 TFLOP/s against 1223 of a large library
+// product: bound by the matrix units and their clock under load.  One token, 4k,
+// 64 heads: 13.8 and 5.2 us, a chain of latencies (the item, its queries, page
+// numbers, keys, two steps, partial results).
 #include "dev_attn.h"
 
 namespace coli {

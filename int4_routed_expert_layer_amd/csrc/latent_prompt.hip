@@ -14,8 +14,8 @@
 // is free as long as V^T (transposed LDS reads) takes them in the same order.
 // Softmax statistics never leave the wave, and the only barrier is the one
 // that turns the ring.  Workgroups of 256 rows, whose steps are copied half as
-// often, gain 6% at 16384 rows and lose as much at 4 x 4096 and 20% on short
-// ragged prompts; the wide head's division of the work (below) loses 15% here.
+// often, gain 6% at 16384 rows and lose 2% at 4 x 4096 and 20% on short ragged
+// prompts; the wide head's division of the work (below) loses 15% here.
 //
 // Measured, bf16: 16384 rows, 16 heads: 1.34 ms, 1025 TFLOP/s, against 1223 of a
 // large library product: bound by the matrix units and their clock under
@@ -334,12 +334,7 @@ __device__ __forceinline__ bool find_tile(const PromptArgs &a, int tiles_cap, in
             if (q0 >= 0 && q1 >= q0 && q1 <= a.n_q) n = (q1 - q0 + kRows - 1) / kRows;
             else bad_seq = true;
         }
-        int cum = n;
-#pragma unroll
-        for (int o = 1; o < 64; o <<= 1) {
-            const int y = __shfl_up(cum, o, 64);
-            if (lane >= o) cum += y;
-        }
+        const int cum = dev::running_sum(n);
         const uint64_t hit = __ballot(done + cum > want);
         if (hit) {
             const int at = __ffsll(static_cast<unsigned long long>(hit)) - 1;
@@ -469,7 +464,10 @@ __global__ __launch_bounds__(256, 2) void latent_prompt_kernel(PromptArgs a, int
     dev::lds_barrier();
     const bool again = bad[0] | bad[1] | bad[2] | bad[3];
     dev::lds_barrier();
-    if (again) attend<BF, NOPE, V, true>(a, tile, s_kv, kv_lds, acc, m, l);
+    if (again) {
+        attend<BF, NOPE, V, true>(a, tile, s_kv, kv_lds, acc, m, l);
+        dev::lds_barrier();                               // the ring is read no more
+    }
 
     const int row = 32 * wave + l31;
     l = dev::sum_halves(l);
@@ -480,12 +478,13 @@ __global__ __launch_bounds__(256, 2) void latent_prompt_kernel(PromptArgs a, int
         return;
     }
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-    const int64_t out_row = static_cast<int64_t>(tile.q0 + tile.row0 + row) * a.n_heads + tile.head;
-    uint8_t *o = row < tile.rows ? a.out + out_row * V * 2 : nullptr;
+    const int64_t first = static_cast<int64_t>(tile.q0 + tile.row0 + 32 * wave) * a.n_heads + tile.head;
 #pragma unroll
-    for (int cb = 0; cb < V / 32; ++cb) dev::store_tile16<BF>(acc[cb], inv, o ? o + 64 * cb : nullptr);
+    for (int cb = 0; cb < V / 32; cb += 2)
+        dev::store_rows16<BF>(acc[cb], acc[cb + 1], inv, s_kv + 1024 + wave * kBlockBytes, a.out + first * V * 2 + 64 * cb,
+                              static_cast<int64_t>(a.n_heads) * V * 2, tile.rows - 32 * wave);
     if (a.lse && lh == 0 && row < tile.rows)
-        a.lse[out_row] = l == 0.0f ? -__builtin_inff() : (m + __builtin_amdgcn_logf(l)) * kLn2;
+        a.lse[first + static_cast<int64_t>(l31) * a.n_heads] = l == 0.0f ? -__builtin_inff() : (m + __builtin_amdgcn_logf(l)) * kLn2;
 }
 
 // ---- The wide head: scoring and summing waves ------------------------------
@@ -786,9 +785,10 @@ __global__ __launch_bounds__(kSplitThreads, 2) void latent_prompt_split_kernel(P
         for (int rb = 0; rb < 4; ++rb) {
             const int row = 32 * rb + l31;
             const float l = s_sum[row], inv = l == 0.0f ? 0.0f : 1.0f / l;
-            uint8_t *o = row < tile.rows ? a.out + ((first + static_cast<int64_t>(row) * a.n_heads) * V + (wave & 3) * (V / 4)) * 2 : nullptr;
-#pragma unroll
-            for (int cb = 0; cb < V / 128; ++cb) dev::store_tile16<BF>(acc[cb][rb], inv, o ? o + 64 * cb : nullptr);
+            static_assert(V == 256);                      // two blocks of columns a wave
+            dev::store_rows16<BF>(acc[0][rb], acc[1][rb], inv, s_kv + (wave & 3) * kBlockBytes,
+                                  a.out + ((first + 32ll * rb * a.n_heads) * V + (wave & 3) * (V / 4)) * 2,
+                                  static_cast<int64_t>(a.n_heads) * V * 2, tile.rows - 32 * rb);
         }
     }
 }

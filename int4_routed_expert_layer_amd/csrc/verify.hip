@@ -31,7 +31,7 @@ constexpr int kSampleThreads = 256, kWalkThreads = 1024;
 // walk, which says which row of p it meets.  Slices are one to four chunks,
 // as many as let every workgroup (five fit a CU) start at once: each makes the
 // walk again.  64 sequences of 151643 fp32 probabilities, 78 MB: two chunks 22 us,
-// 3.5 TB/s, of which the walk and the meeting take 6; one chunk (two rounds of
+// 3.5 TB/s, of which the walk takes 3.6 us; one chunk (two rounds of
 // workgroups) 31.5 us; 16384 elements in 16 rounds of one group 24.3 us.
 constexpr int kGroups = 4;
 constexpr int kChunk = kSampleThreads * 4 * kGroups;
