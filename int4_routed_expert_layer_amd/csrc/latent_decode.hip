@@ -429,7 +429,7 @@ __global__ __launch_bounds__(kThreads, 2) void latent_decode_kernel(DecodeArgs a
     __shared__ float s_red[2 * 2 * kTileRows], s_fac[kTileRows], s_sum[2 * kTileRows];
     __shared__ int s_raise[3], s_bad;
     const int tid = threadIdx.x, lane = tid & 63, wave = dev::wave_id();
-    const int l31 = lane & 31, lh = lane >> 5;
+    const int l31 = lane & 31;
     const uint32_t kv_lds = dev::lds_address(s_kv);
 
     // The two kinds walk the items in loops of their own (and meet at the same
@@ -592,6 +592,7 @@ constexpr int kItemCost = 3;    // tiles: the queries, the first tile's latency 
 constexpr int kJoinItems = 64;  // pieces whose joining costs as much as a tile
 constexpr int kMinRun = 2;
 constexpr int kSortMost = 1024; // sequences that are put in order
+constexpr int kItemLanes = 16;  // lanes that write a sequence's items
 
 __device__ __forceinline__ int cut(int tiles, int per) { return max(1, (tiles + per - 1) / per); }
 
@@ -600,7 +601,11 @@ __global__ __launch_bounds__(kPlanThreads) void decode_plan_kernel(DecodePlan p,
                                                                    int32_t *err) {
     __shared__ int s_tmp[kPlanThreads / 64 + 1];
     __shared__ unsigned long long s_units, s_work;
-    __shared__ int s_most, s_count[kPlanThreads / 64], s_key[kSortMost], s_order[kSortMost];
+    __shared__ int s_most, s_count[kPlanThreads / 64], s_order[kSortMost];
+    __shared__ __align__(16) int s_key[kSortMost];
+    // What the first sequences need, nearer than device memory: units, tiles,
+    // first item and slot, and first token, tokens, length.
+    __shared__ int4 s_seq[kSortMost], s_at[kSortMost];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     int4 *seq = reinterpret_cast<int4 *>(p.seq);         // units, tiles, first item, first slot
     if (tid == 0) {
@@ -609,16 +614,34 @@ __global__ __launch_bounds__(kPlanThreads) void decode_plan_kernel(DecodePlan p,
     }
     __syncthreads();
     bool bad = false;
+    unsigned long long my_units = 0, my_work = 0;
+    int my_most = 1;
     for (int b = tid; b < n_seq; b += kPlanThreads) {
         const int q0 = q_start[b], q1 = q_start[b + 1], len = kv_len[b];
         const bool ok = q0 >= 0 && q1 >= q0 && q1 <= n_tok && len >= 0 && len <= INT32_MAX - 2 * kTileKeys;
         bad = bad || !ok;
         const int units = ok ? static_cast<int>((static_cast<int64_t>(q1 - q0) * n_heads + kTileRows - 1) / kTileRows) : 0;
         const int tiles = ok ? (len + kTileKeys - 1) / kTileKeys : 0;
-        seq[b] = int4{units, tiles, 0, 0};
-        atomicAdd(&s_units, static_cast<unsigned long long>(units));
-        atomicAdd(&s_work, static_cast<unsigned long long>(units) * tiles);
-        if (units) atomicMax(&s_most, tiles);
+        if (b < kSortMost) {
+            s_seq[b] = int4{units, tiles, 0, 0};
+            s_at[b] = int4{q0, q1 - q0, len, 0};
+        } else {
+            seq[b] = int4{units, tiles, 0, 0};
+        }
+        my_units += units;
+        my_work += static_cast<unsigned long long>(units) * tiles;
+        if (units) my_most = max(my_most, tiles);
+    }
+#pragma unroll
+    for (int o = 32; o; o >>= 1) {
+        my_units += __shfl_xor(my_units, o, 64);
+        my_work += __shfl_xor(my_work, o, 64);
+        my_most = max(my_most, __shfl_xor(my_most, o, 64));
+    }
+    if (lane == 0) {
+        atomicAdd(&s_units, my_units);
+        atomicAdd(&s_work, my_work);
+        atomicMax(&s_most, my_most);
     }
     __syncthreads();
     const unsigned long long units = s_units;
@@ -627,13 +650,15 @@ __global__ __launch_bounds__(kPlanThreads) void decode_plan_kernel(DecodePlan p,
         bad = true;
         n_seq = 0;
     }
-    // Items at a run length, one wave per candidate.
+    // Items at a run length, one wave per candidate; 2^24 stands for any more.
     auto items_at = [&](int per) {
         unsigned long long n = 0;
-        for (int b = lane; b < n_seq; b += 64) n += static_cast<unsigned long long>(seq[b].x) * cut(seq[b].y, per);
-#pragma unroll
-        for (int o = 32; o; o >>= 1) n += __shfl_xor(n, o, 64);
-        return n;
+        for (int b = lane; b < n_seq; b += 64) {
+            const int4 s = b < kSortMost ? s_seq[b] : seq[b];
+            n += static_cast<unsigned long long>(s.x) * cut(s.y, per);
+        }
+        const int sum = dev::running_sum(static_cast<int>(min(n, 1ull << 24)));
+        return static_cast<unsigned long long>(__builtin_amdgcn_readlane(sum, 63));
     };
     int best = 0;
     long long best_cost = 0;
@@ -641,14 +666,19 @@ __global__ __launch_bounds__(kPlanThreads) void decode_plan_kernel(DecodePlan p,
         const unsigned long long room = static_cast<unsigned long long>(r) * n_cu;
         if (units > room) continue;
         int lo = min(kMinRun, most), hi = most;          // items_at(hi) == units <= room
+        // work / run <= items <= work / run + units: what that leaves of the range,
+        // with room for the roundings of the fp32 quotients.
+        const float work = static_cast<float>(s_work);
+        lo = static_cast<int>(fminf(fmaxf(0.9999f * work / static_cast<float>(room) - 1.0f, static_cast<float>(lo)), static_cast<float>(hi)));
+        if (units < room) hi = max(lo, static_cast<int>(fminf(1.0001f * work / static_cast<float>(room - units) + 2.0f, static_cast<float>(hi))));
         while (lo < hi) {
             const int step = (hi - lo + 15) / 16;        // candidates lo + step * wave
             const int mine = min(lo + step * wave, hi);
             const bool fits = items_at(mine) <= room;
             if (lane == 0) s_count[wave] = fits;
             __syncthreads();
-            int w = 0;
-            while (w < 16 && !s_count[w]) ++w;           // fits is monotone in the run length
+            // The first that fits: fits is monotone in the run length.
+            const int w = __ffsll(__ballot(lane >= kPlanThreads / 64 || s_count[lane])) - 1;
             __syncthreads();
             const int top = w < 16 ? min(lo + step * w, hi) : hi;
             lo = w == 0 ? lo : min(lo + step * (w - 1) + 1, top);
@@ -669,16 +699,20 @@ __global__ __launch_bounds__(kPlanThreads) void decode_plan_kernel(DecodePlan p,
     const bool sorted = n_seq <= kSortMost && items_at(best) > static_cast<unsigned long long>(n_cu);
     __syncthreads();
     if (sorted) {
-        int mine = 0;
+        // By length, then by number, in one value (runs of 2^21 tiles or more tie).
+        int mine = -1;
         if (tid < n_seq) {
-            const int split = cut(seq[tid].y, best);
-            mine = (seq[tid].y + split - 1) / split;
-            s_key[tid] = mine;
+            const int tiles = s_seq[tid].y, split = cut(tiles, best);
+            mine = min((tiles + split - 1) / split, (1 << 21) - 1) * kSortMost + kSortMost - 1 - tid;
         }
+        s_key[tid] = mine;
         __syncthreads();
         if (tid < n_seq) {
             int rank = 0;
-            for (int b = 0; b < n_seq; ++b) rank += s_key[b] > mine || (s_key[b] == mine && b < tid);
+            for (int b = 0; b < n_seq; b += 4) {
+                const int4 k = *reinterpret_cast<const int4 *>(s_key + b);
+                rank += (k.x > mine) + (k.y > mine) + (k.z > mine) + (k.w > mine);
+            }
             s_order[rank] = tid;
         }
     }
@@ -687,7 +721,7 @@ __global__ __launch_bounds__(kPlanThreads) void decode_plan_kernel(DecodePlan p,
     __syncthreads();
     for (int b0 = 0; b0 < n_seq; b0 += kPlanThreads) {
         const int b = b0 + tid >= n_seq ? n_seq : sorted ? s_order[b0 + tid] : b0 + tid;
-        int4 s = b < n_seq ? seq[b] : int4{0, 0, 0, 0};
+        int4 s = b >= n_seq ? int4{0, 0, 0, 0} : b < kSortMost ? s_seq[b] : seq[b];
         const int split = cut(s.y, best), count = s.x * split;
         int total;
         const int at = n_items + dev::block_exclusive_scan<kPlanThreads>(count, s_tmp, &total);
@@ -699,10 +733,11 @@ __global__ __launch_bounds__(kPlanThreads) void decode_plan_kernel(DecodePlan p,
         if (b < n_seq) {
             s.z = at;
             s.w = split > 1 ? slot : -1;
-            seq[b] = s;
+            if (b < kSortMost) s_seq[b] = s;
+            else seq[b] = s;
             if (split > 1 && s.x) atomicMax(&s_most, split);
             if (split > 1 && slot + count <= p.slot_cap && join + s.x <= p.join_cap) {
-                const int q0 = q_start[b], rows = (q_start[b + 1] - q0) * n_heads;
+                const int q0 = b < kSortMost ? s_at[b].x : q_start[b], rows = (b < kSortMost ? s_at[b].y : q_start[b + 1] - q0) * n_heads;
                 for (int i = 0; i < s.x; ++i)
                     p.joins[join + i] = JoinUnit{q0 * n_heads + i * kTileRows, min(kTileRows, rows - i * kTileRows), slot + i * split, split};
             }
@@ -729,20 +764,27 @@ __global__ __launch_bounds__(kPlanThreads) void decode_plan_kernel(DecodePlan p,
         }
     }
     if (fits)
-        for (int b = wave; b < n_seq; b += kPlanThreads / 64) {
-            const int4 s = seq[b];
-            const int split = cut(s.y, best), q0 = q_start[b], n = q_start[b + 1] - q0, len = kv_len[b];
+        for (int b = tid / kItemLanes; b < n_seq; b += kPlanThreads / kItemLanes) {
+            int4 s, at;
+            if (b < kSortMost) {
+                s = s_seq[b];
+                at = s_at[b];
+            } else {
+                s = seq[b];
+                at = int4{q_start[b], q_start[b + 1] - q_start[b], kv_len[b], 0};
+            }
+            const int split = cut(s.y, best), each = s.y / split, over = s.y - each * split;
             // Neighbouring items: the units of one run of keys.
-            for (int i = lane; i < s.x * split; i += 64) {
+            for (int i = tid % kItemLanes; i < s.x * split; i += kItemLanes) {
                 const int c = i / s.x, u = i - c * s.x;
                 DecodeItem it;
-                it.q0 = q0;
-                it.n = n;
-                it.len = len;
+                it.q0 = at.x;
+                it.n = at.y;
+                it.len = at.z;
                 it.seq = b | ((s.z + i) / n_cu + 1 < rounds ? kItemMore : 0);
                 it.row0 = u * kTileRows;
-                it.t0 = static_cast<int>(static_cast<int64_t>(s.y) * c / split);
-                it.t1 = static_cast<int>(static_cast<int64_t>(s.y) * (c + 1) / split);
+                it.t0 = c * each + min(c, over);
+                it.t1 = it.t0 + each + (c < over);
                 it.slot = s.w < 0 ? -1 : s.w + u * split + c;
                 p.items[place(s.z + i)] = it;
             }
