@@ -581,7 +581,12 @@ __global__ __launch_bounds__(256) void join_kernel(DecodeArgs a) {
 // The plan of a step, by one workgroup: each sequence's rows are cut into
 // 64-row units and its key tiles into runs of at most `per`, the run length
 // with the shortest estimated time.  One round over the CUs: the smallest run
-// length that gives no more items than CUs, and takes as long as that.  Two to
+// length that gives no more items than CUs, or a longer one, whose fewer pieces
+// are joined the sooner: 16 pieces of one sequence, which a workgroup has in
+// flight together, take most of a tile's time, and each piece a share of it (one
+// token, 4096 keys: runs of two tiles 19.3 us, of four 20.3; 16384: two 36.3, four
+// 28.7; 32768: two 50.9, eight 34.7; 16 tokens of 1000: two 27.7, four 24.4; 64 of
+// 1000: four to eight 36.8, undivided 53.7).  Two to
 // four rounds: the smallest that fits them; the sequences are then taken in the
 // order of their runs' lengths and every other round is laid out backwards, so
 // that the CUs' sums come close to their mean (16 ragged trees of 25 nodes:
@@ -594,6 +599,7 @@ constexpr int kPlanThreads = 1024;
 constexpr int kItemCost = 3;    // tiles: the queries, the first tile's latency and the partial result
 constexpr int kJoinItems = 64;  // pieces whose joining costs as much as a tile
 constexpr int kMinRun = 2;
+constexpr float kTileTime = 1.4f, kPieceTime = 0.06f;   // of 16 pieces' joining
 constexpr int kSortMost = 1024; // sequences that are put in order
 constexpr int kItemLanes = 16;  // lanes that write a sequence's items
 
@@ -604,6 +610,7 @@ __global__ __launch_bounds__(kPlanThreads) void decode_plan_kernel(DecodePlan p,
                                                                    int32_t *err) {
     __shared__ int s_tmp[kPlanThreads / 64 + 1];
     __shared__ unsigned long long s_units, s_work;
+    __shared__ float s_cost[kPlanThreads / 64];
     __shared__ int s_most, s_count[kPlanThreads / 64], s_order[kSortMost];
     __shared__ __align__(16) int s_key[kSortMost];
     // What the first sequences need, nearer than device memory: units, tiles,
@@ -686,6 +693,22 @@ __global__ __launch_bounds__(kPlanThreads) void decode_plan_kernel(DecodePlan p,
             const int top = w < 16 ? min(lo + step * w, hi) : hi;
             lo = w == 0 ? lo : min(lo + step * (w - 1) + 1, top);
             hi = top;
+        }
+        if (r == 1) {
+            // The smallest that fits, or one up to 4.75 times as long whose fewer
+            // pieces are joined the sooner.
+            const int mine = static_cast<int>(min(hi + static_cast<long long>(hi) * wave / 4, static_cast<long long>(most)));
+            const unsigned long long n = items_at(mine);
+            const int depth = cut(most, mine);
+            const float cost = kTileTime * static_cast<float>(mine) + (n == units ? 0.0f : static_cast<float>((depth + 15) / 16) + kPieceTime * static_cast<float>(n));
+            if (lane == 0) s_cost[wave] = cost;
+            __syncthreads();
+            const float mycost = s_cost[lane & 15];
+            float least = mycost;
+#pragma unroll
+            for (int o = 8; o; o >>= 1) least = fminf(least, __shfl_xor(least, o, 64));
+            const int w = __ffsll(__ballot(mycost == least)) - 1;
+            hi = static_cast<int>(min(hi + static_cast<long long>(hi) * w / 4, static_cast<long long>(most)));
         }
         const long long items = static_cast<long long>(items_at(hi));
         const long long each = r == 1 ? hi : max(static_cast<long long>(hi), static_cast<long long>(s_work / n_cu) + hi / 8);
