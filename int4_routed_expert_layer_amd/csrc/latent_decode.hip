@@ -29,13 +29,13 @@
 // pieces leave unnormalised sums, maxima and fp32 partial outputs, which
 // join_kernel combines.
 //
-// Measured.  64 tokens of sequences up to 12k, 64 heads, bf16: 68 us and 9 for the
-// join, 352 MB, 5.2 TB/s in the first: bound by HBM.  Four chains of four tokens up
-// to 128k, 16 heads, f16: 96 and 12 us, 535 MB, 5.6 TB/s.  16 trees of 25 nodes up
-// to 5k, 64 heads, bf16: 153 us, 940 TFLOP/s against 1223 of a large library
+// Measured.  64 tokens of sequences up to 12k, 64 heads, bf16: 66 us and 9 for the
+// join, 352 MB, 5.3 TB/s in the first: bound by HBM.  Four chains of four tokens up
+// to 128k, 16 heads, f16: 93 and 12 us, 535 MB, 5.8 TB/s.  16 trees of 25 nodes up
+// to 5k, 64 heads, bf16: 149 us, 960 TFLOP/s against 1223 of a large library
 // product: bound by the matrix units and their clock under load.  One token, 4k,
-// 64 heads: 13.8 and 5.2 us, a chain of latencies (the item, its queries, page
-// numbers, keys, two steps, partial results).
+// 64 heads: 11 and 5 us, a chain of latencies (the item, its queries, page numbers,
+// keys, four steps, partial results).
 #include "dev_attn.h"
 
 namespace coli {
@@ -129,15 +129,31 @@ __device__ __forceinline__ void score_item(const DecodeArgs &a, const DecodeItem
     int node[2];
     u32x4 q[kDepth][2];
 #pragma unroll
-    for (int rb = 0; rb < 2; ++rb) {
-        const int rr = it.row0 + min(row + 16 * rb, rows - 1);
-        node[rb] = rr / a.n_heads;
-        const int head = rr - node[rb] * a.n_heads;
-        const int64_t tok = it.q0 + node[rb];
-        const uint8_t *ql = a.q_lat + (tok * a.ql_tok + head * a.ql_head) * 2 + 16 * lq;
-        const uint8_t *qp = a.q_pe + (tok * a.qp_tok + head * a.qp_head) * 2 + 16 * lq;
+    for (int rb = 0; rb < 2; ++rb) node[rb] = (it.row0 + min(row + 16 * rb, rows - 1)) / a.n_heads;
+    if (sh.t0 < sh.t1) {
+        // The queries come by way of the ring's last two places, each row once and
+        // whole, which leaves the keys' copies room: loaded by each wave as
+        // its products take them, they let the first step begin 11400 clocks after
+        // the item, so 3900 (one token, 4096 keys 19.9 -> 16.9 us).
+        const int r = 8 * wave + (lane >> 3), unit = ((lane & 7) ^ dev::tile_swz(r)) << 4;
+        const uint32_t at = dev::lds_address(sh.kv) + 2 * kStepBytes + wave * 1024;
 #pragma unroll
-        for (int k = 0; k < kDepth; ++k) q[k][rb] = dev::gload<u32x4>(k < kLatent / 32 ? ql + 64 * k : qp + 64 * (k - kLatent / 32));
+        for (int h = 0; h < 2; ++h) {
+            const int rr = it.row0 + min(r + 32 * h, rows - 1), n = rr / a.n_heads, head = rr - n * a.n_heads;
+            const int64_t tok = it.q0 + n;
+            const uint8_t *ql = a.q_lat + (tok * a.ql_tok + head * a.ql_head) * 2 + unit;
+            const uint8_t *qp = a.q_pe + (tok * a.qp_tok + head * a.qp_head) * 2 + unit;
+#pragma unroll
+            for (int b = 0; b < kBlocks; ++b)
+                dev::copy16_to_lds_free(b < kLatentBlocks ? ql + 128 * b : qp, at + h * kStepBytes + b * kBlockBytes);
+        }
+        dev::copy_barrier();
+        const uint8_t *mine = sh.kv + (2 + wm) * kStepBytes;
+#pragma unroll
+        for (int k = 0; k < kDepth; ++k)
+#pragma unroll
+            for (int rb = 0; rb < 2; ++rb)
+                q[k][rb] = *reinterpret_cast<const u32x4 *>(mine + (k >> 1) * kBlockBytes + dev::tile_unit(l15 + 16 * rb, 4 * (k & 1) + lq));
     }
     __builtin_amdgcn_s_setprio(2);   // the step waits for these waves: the summing ones fill what they leave
     m[0] = m[1] = -__builtin_inff();
@@ -387,11 +403,14 @@ __device__ __forceinline__ void sum_item(const DecodeArgs &a, const DecodeItem &
 
     const int pg0 = page_of(sh.t0), pg1 = page_of(sh.t0 + 1), pg2 = page_of(sh.t0 + 2), pg3 = page_of(sh.t0 + 3);
     int page = page_of(sh.t0 + 4);
-#pragma unroll 1
-    for (int i = 0; i < 3; ++i) copy_all(aim(sh.t0 + i, i == 0 ? pg0 : i == 1 ? pg1 : pg2));
-    Copy now = aim(sh.t0 + 3, pg3);
-    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * kBlocks) : "memory");
-    dev::lds_barrier();                                  // step t0 has landed
+    copy_all(aim(sh.t0, pg0));
+    copy_all(aim(sh.t0 + 1, pg1));
+    Copy now = aim(sh.t0 + 2, pg2);
+    dev::lds_barrier();                                  // the queries have landed
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kBlocks) : "memory");
+    dev::lds_barrier();                                  // step t0 has landed, and the queries have been read
+    copy_all(now);
+    now = aim(sh.t0 + 3, pg3);
     dev::lds_barrier();                                  // the first maxima
     for (int t = sh.t0 + 1; t < sh.t1; ++t) {
         // Step t has landed when only the copies of step t + 1 are in flight.
