@@ -196,6 +196,14 @@ def test_strided_queries_and_pages_of_an_interleaved_cache():
     s.close()
 
 
+@pytest.mark.parametrize("longest,heads", [(150, 16), (900, 65)])
+def test_more_sequences_than_a_workgroup_has_threads(longest, heads):
+    """1100 sequences, some of them empty: the plan takes them in turns."""
+    lens = [int(x) for x in np.random.default_rng(21).integers(0, longest, 1100)]
+    c = Case(lens, [min(n, 1) for n in lens], heads, 64, seed=21)
+    c.check(*c.run(), heads=[heads // 2])
+
+
 def test_on_another_stream_and_replayed_from_a_graph():
     c = Case([600, 90], [2, 3], 16, 16, seed=13)
     want, want_lse = c.run()

@@ -150,6 +150,30 @@ def test_values_that_are_not_finite_in_divided_keys(width):
 
 
 @pytest.mark.parametrize("width", ["wide", "narrow"])
+def test_divided_keys_on_another_stream_and_replayed_from_a_graph(width):
+    c = Case([90, 20], [1000, 700], 3, width, seed=13)
+    want, want_lse = c.run()
+    s = Serve(3, 110, 2, nope=c.nope, v_dim=c.v)
+    args = [x.to(DEV) for x in (c.q, c.kv, c.pe, c.qs, c.ks)]
+    out, lse = torch.empty_like(want), torch.empty_like(want_lse)
+    torch.cuda.synchronize()
+    st = torch.cuda.Stream()
+    with torch.cuda.stream(st):
+        s.prompt(*args, c.scale, out=out, lse=lse)
+    st.synchronize()
+    assert torch.equal(out, want) and torch.equal(lse, want_lse)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        s.prompt(*args, c.scale, out=out, lse=lse)
+    for _ in range(3):
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and torch.equal(lse, want_lse)
+    s.close()
+
+
+@pytest.mark.parametrize("width", ["wide", "narrow"])
 def test_many_sequences_and_uncovered_tokens(width):
     n = [int(x) for x in np.random.default_rng(6).integers(0, 40, 150)]
     c = Case(n, n, 1, width, seed=6)
