@@ -97,7 +97,7 @@ class Serve:
     def _rows(self, name, t, dtype, shape):
         """Address of a tensor of this type and shape whose last dimension is contiguous."""
         try:
-            if t.dtype is dtype and t.shape == shape and t.get_device() == self.index and (t.stride(-1) == 1 or t.shape[-1] <= 1):
+            if t.dtype is dtype and t.shape == shape and t.get_device() == self.index and (t.stride()[-1] == 1 or t.shape[-1] <= 1):
                 return t.data_ptr()
         except (AttributeError, IndexError):
             pass
@@ -136,7 +136,7 @@ class Serve:
 
     def _table(self, block_table, n_seq):
         cols = self._sizes("block_table", block_table, 2)[1]
-        return self._rows("block_table", block_table, torch.int32, (n_seq, cols)), block_table.stride(0), cols
+        return self._rows("block_table", block_table, torch.int32, (n_seq, cols)), block_table.stride()[0], cols
 
     def _out(self, name, out, shape, dtype):
         """An output tensor and its address."""
@@ -177,7 +177,7 @@ class Serve:
             q_out, po = self._out("q_out", q_out, shape, self.dtype)
         elif q_out is not None:
             raise ValueError("q_out without q_pe")
-        self._call(_append, pc, c.stride(0), pw, eps, pcos, psin, n_pos, 1 if interleaved else 0, ppos, pslot, n, base, page, pages, pq, qt, qh, po)
+        self._call(_append, pc, c.stride()[0], pw, eps, pcos, psin, n_pos, 1 if interleaved else 0, ppos, pslot, n, base, page, pages, pq, qt, qh, po)
         return q_out
 
     def plan(self, q_start, kv_len, n_tok=None):
@@ -239,7 +239,7 @@ class Serve:
             lse, pe = self._out("lse", lse, (n_q, h), torch.float32)
         qt, qh, _ = q.stride()
         kt, kh, _ = kv.stride()
-        self._call(_prompt, pq, qt, qh, pkv, kt, kh, pk, k_pe.stride(0), ps, pks, n_seq, n_q, n_k, 1 if causal else 0, scale, po, pe)
+        self._call(_prompt, pq, qt, qh, pkv, kt, kh, pk, k_pe.stride()[0], ps, pks, n_seq, n_q, n_k, 1 if causal else 0, scale, po, pe)
         return out if pe is None else (out, lse)
 
     def verify(self, probs, tokens, q_start, u, race, draft_probs=None, parents=None, max_path=None):
@@ -272,7 +272,7 @@ class Serve:
         count = torch.empty(n_seq, dtype=torch.int32, device=self.device)
 
         def rows(t):   # a tensor of one row may have any row stride
-            return t.stride(0) if t.shape[0] > 1 else vocab
+            return t.stride()[0] if t.shape[0] > 1 else vocab
 
         self._call(_verify, pp, rows(probs), pd, 0 if pd is None else rows(draft_probs), kind, vocab, pt, pa, ps, n_seq, n, pu, pr, rows(race),
                    path.data_ptr(), cols, count.data_ptr(), nxt.data_ptr())
@@ -284,7 +284,7 @@ class Serve:
         layer in one launch; path int32 [B, cols] as ``verify`` returns it."""
         layers, layer_stride, lead = 1, 0, ()
         if isinstance(cache, torch.Tensor) and cache.dim() == 4:
-            layers, layer_stride = cache.shape[0], cache.stride(0)
+            layers, layer_stride = cache.shape[0], cache.stride()[0]
             lead = (layers,)
             if layers == 0:
                 return
@@ -295,7 +295,7 @@ class Serve:
         most = self._sizes("path", path, 2)[1]
         pp = self._rows("path", path, torch.int32, (n_seq, most))
         self._call(_keep, base, page, pages, layers, layer_stride, table, row, cols, ps, pl, n_seq, self.dims.max_tokens if n_tok is None else n_tok,
-                   pp, path.stride(0), most)
+                   pp, path.stride()[0], most)
 
     def device_errors(self) -> int:
         """Read and clear the device error flags (synchronises the device)."""
