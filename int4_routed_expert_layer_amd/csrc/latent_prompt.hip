@@ -804,7 +804,13 @@ template <typename K, typename J>
 hipError_t launch_tiles(PromptArgs &a, K kernel, J join, int threads, int blocks, int places, hipStream_t s) {
     const int64_t seqs = std::min(a.n_seq, a.n_q), cap = (a.n_q - seqs) / kRows + seqs, tiles = cap * a.n_heads;
     const int64_t most = (a.n_k + kStepKeys - 1) / kStepKeys / kLeastSteps;
-    a.split = static_cast<int>(std::max<int64_t>(1, std::min({std::min(places, a.part_cap) / tiles, most, kMostParts})));
+    // Without much context the first tiles see few keys and the last most: two
+    // rounds of parts even that out, where they are of 24 steps or more (4096
+    // rows, 12 narrow heads: 127 us in one round, 102 in two; 6 wide heads 114 and 87;
+    // but 1024 rows, 32 narrow heads: 34 and 39).
+    const int64_t even = a.causal && a.n_k < 2ll * a.n_q ? std::min<int64_t>(2 * places, a.part_cap) / tiles : 0;
+    const int64_t want = std::max<int64_t>(std::min(places, a.part_cap) / tiles, std::min<int64_t>(even, a.n_k / a.n_seq / (24 * kStepKeys)));
+    a.split = static_cast<int>(std::max<int64_t>(1, std::min({want, most, kMostParts})));
     const int64_t grid = (tiles * a.split + 7) / 8 * 8;
     if (grid > INT32_MAX) return hipErrorInvalidValue;
     launch(kernel, static_cast<unsigned>(grid), threads, 0, s, a, static_cast<int>(cap));

@@ -64,7 +64,7 @@ struct DecodeArgs {
     DecodePlan plan;
     int join_most;             // at least the plan's join units
     float *part;               // [slot_cap x 64 x 512], in the order of join_kernel's blocks
-    float *part_ml;            // [slot_cap x 64 x 2]
+    float *part_ml;            // [slot_cap x 64 x 2], with room for part_cap of the prompts
     int32_t *err;
 };
 

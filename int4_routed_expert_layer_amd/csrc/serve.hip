@@ -65,6 +65,10 @@ struct OnDevice {
 
 bool aligned(const void *p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 
+// Floats of statistics per row of a slot: two for absorbed attention, up to eight for
+// expanded, whose parts have fewer outputs.
+constexpr int kSlotStats = 8;
+
 struct Sizes {
     int64_t items, joins, slots, seqs;
 };
@@ -80,7 +84,7 @@ Sizes plan_sizes(const coli_serve_dims &d, int n_cu) {
 size_t create_bytes(const coli_serve_dims &d, int n_cu) {
     const Sizes z = plan_sizes(d, n_cu);
     return static_cast<size_t>(z.items) * sizeof(DecodeItem) + static_cast<size_t>(z.joins) * sizeof(JoinUnit) +
-           static_cast<size_t>(z.slots) * kTileRows * (kLatent + 2) * sizeof(float) +
+           static_cast<size_t>(z.slots) * kTileRows * (kLatent + kSlotStats) * sizeof(float) +
            static_cast<size_t>(z.seqs) * (8 * sizeof(int32_t) + 2 * sizeof(uint64_t) + sizeof(int32_t)) + 4 * sizeof(int32_t);
 }
 
@@ -175,7 +179,7 @@ coli_status coli_serve_create(const coli_serve_dims *d, int device, coli_serve *
         {reinterpret_cast<void **>(&S->plan.joins), z.joins * sizeof(JoinUnit), "plan joins"},
         {reinterpret_cast<void **>(&S->plan.seq), z.seqs * 4 * sizeof(int32_t), "plan scratch"},
         {reinterpret_cast<void **>(&S->part), z.slots * kTileRows * kLatent * sizeof(float), "partial outputs"},
-        {reinterpret_cast<void **>(&S->part_ml), z.slots * kTileRows * 2 * sizeof(float), "partial statistics"},
+        {reinterpret_cast<void **>(&S->part_ml), z.slots * kTileRows * kSlotStats * sizeof(float), "partial statistics"},
         {reinterpret_cast<void **>(&S->walk), z.seqs * 4 * sizeof(int32_t), "draft walks"},
         {reinterpret_cast<void **>(&S->best), z.seqs * 2 * sizeof(uint64_t), "sample maxima"},
         {reinterpret_cast<void **>(&S->arrived), z.seqs * sizeof(int32_t), "arrival counters"},
@@ -376,7 +380,8 @@ coli_status coli_latent_prompt(coli_serve *S, const void *q, int64_t q_tok_strid
     a.lse = lse;
     a.part = S->part;
     a.part_ml = S->part_ml;
-    a.part_cap = S->plan.slot_cap / 2;   // two 64 x 512 slots hold a part of 128 rows and up to 256 columns, with its statistics
+    // Parts of 128 rows that the slots hold: by their outputs, and by their statistics.
+    a.part_cap = std::min(S->plan.slot_cap * (kTileRows * kLatent / 128) / S->d.v_dim, S->plan.slot_cap * (kTileRows * kSlotStats / 256));
     a.err = S->err;
     OnDevice on(S->device);
     return launched(S, launch_latent_prompt(a, S->d.half == COLI_HALF_BF16, S->d.nope, S->n_cu, static_cast<hipStream_t>(stream)), "prompt launch");
