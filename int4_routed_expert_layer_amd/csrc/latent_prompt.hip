@@ -8,16 +8,20 @@
 //
 // The narrow head: a wave takes 32 query rows of one head and walks the keys in
 // steps of 32 that its workgroup copies straight into LDS, a ring of three; two
-// waves share a SIMD, of workgroups of their own.  S^T = K Q^T leaves lane L with row L % 32 of its wave
-// and half of the keys; rounded to 16 bits those registers are the second
-// product's B operand as they stand, because the order of keys inside a K step
-// is free as long as V^T (transposed LDS reads) takes them in the same order.
-// Softmax statistics never leave the wave, and the only barrier is the one
-// that turns the ring.  Probabilities enter the second product in the 16 bits
-// that its instruction takes (their fp32 sum is taken before): bf16 outputs then
-// are off by 2.3e-3 of their size, 1.7e-3 of which is their own rounding.  Workgroups of 256 rows, whose steps are copied half as
-// often, gain 6% at 16384 rows and lose 2% at 4 x 4096 and 20% on short ragged
-// prompts; the wide head's division of the work (below) loses 15% here.
+// waves share a SIMD, of workgroups of their own.  S^T = K Q^T leaves lane L with
+// row L % 32 of its wave and half of the keys; rounded to 16 bits those registers
+// are the second product's B operand as they stand, because the order of keys
+// inside a K step is free as long as V^T (transposed LDS reads) takes them in the
+// same order.  Softmax statistics never leave the wave, and the only barrier is
+// the one that turns the ring.  Probabilities enter the second product in the 16
+// bits that its instruction takes (their fp32 sum is taken before): bf16 outputs
+// then are off by 2.3e-3 of their size, 1.7e-3 of which is their own rounding.
+// Workgroups of 256 rows, whose steps are copied half as often, gain 6% at 16384
+// rows and lose 2% at 4 x 4096 and 20% on short ragged prompts; the wide head's
+// division of the work (below) loses 15% here.
+//
+// A call with few tiles divides the keys of each among workgroups that leave
+// unnormalised sums, maxima and fp32 partial outputs; join_parts_kernel adds them.
 //
 // Measured, bf16: 16384 rows, 16 heads: 1.32 ms, 1043 TFLOP/s, against 1223 of a
 // large library product: bound by the matrix units and their clock under
