@@ -507,8 +507,9 @@ coli_status coli_latent_prompt(coli_serve *serve, const void *q, int64_t q_tok_s
  * Outputs, int32: path [n_seq x path_cols] the nodes taken, node 0 first,
  * then -1; count [n_seq] their number; next_tokens [n_seq x path_cols] the
  * tokens of path[1..] and the sampled one, then -1.  A path longer than path_cols
- * ends there.  A sequence without nodes has count 0.  Probabilities that are
- * negative or NaN count as zero. */
+ * ends there.  A sequence without nodes has count 0.  With n_tok = 0 probs, draft,
+ * tokens, u and race may be NULL.  Probabilities that are negative or NaN count
+ * as zero. */
 coli_status coli_draft_verify(coli_serve *serve, const void *probs, int64_t probs_stride, const void *draft, int64_t draft_stride,
                               int32_t kind, int32_t vocab, const int32_t *tokens, const int32_t *parents, const int32_t *q_start,
                               int32_t n_seq, int32_t n_tok, const float *u, const float *race, int64_t race_stride, int32_t *path,

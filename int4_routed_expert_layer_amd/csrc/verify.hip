@@ -398,11 +398,13 @@ hipError_t launch_kind(const VerifyArgs &a, int n_cu, hipStream_t s) {
     const int64_t want = (static_cast<int64_t>(a.vocab) * a.n_seq + static_cast<int64_t>(kPerCU) * n_cu * kChunk - 1) / (static_cast<int64_t>(kPerCU) * n_cu * kChunk);
     const int chunks = static_cast<int>(std::min<int64_t>(std::max<int64_t>(want, 1), kMostChunks));
     const unsigned slices = static_cast<unsigned>((a.vocab + chunks * kChunk - 1) / (chunks * kChunk));
+    // A call without nodes has only paths of nothing to write: its probabilities
+    // and race may be NULL, and sampling loads race before it knows of any node.
     const bool sums = a.q && a.parents;
-    if (sums) {
+    if (sums || a.n_tok == 0) {
         launch(walk_kernel<K>, static_cast<unsigned>(a.n_seq), kWalkThreads, 0, s, a);
         hipError_t e = hipGetLastError();
-        if (e != hipSuccess) return e;
+        if (e != hipSuccess || a.n_tok == 0) return e;
         launch(sample_kernel<K, true>, dim3(slices, a.n_seq), kSampleThreads, 0, s, a, chunks);
     } else {
         launch(sample_kernel<K, false>, dim3(slices, a.n_seq), kSampleThreads, 0, s, a, chunks);
