@@ -65,10 +65,14 @@ __device__ __forceinline__ void prob4(const uint8_t *row, int i, float (&v)[4]) 
 template <int K>
 constexpr int prob_bytes() { return K == kF32 ? 4 : 2; }
 
-// (p - a q)+, each operation rounded on its own (no fused multiply-add).
+// Negative and NaN probabilities count as zero.
+__device__ __forceinline__ float counted(float v) { return v > 0.0f ? v : 0.0f; }
+
+// (p - a q)+, each operation rounded on its own (no fused multiply-add).  (A p
+// of no value leaves nothing as it stands.)
 __device__ __forceinline__ float residual(float p, float a, float q) {
 #pragma clang fp contract(off)
-    const float t = a * q;
+    const float t = a * counted(q);
     const float r = p - t;
     return r > 0.0f ? r : 0.0f;
 }
@@ -105,8 +109,8 @@ __device__ __forceinline__ Walk walk(const VerifyArgs &a, int t0, int n, Nodes &
         }
         float p = 0.0f, q = 1.0f;
         if (ok) {
-            p = prob<K>(a.p + (t0 + parent) * a.p_stride * prob_bytes<K>(), x);
-            if (a.q) q = prob<K>(a.q + (t0 + parent) * a.q_stride * prob_bytes<K>(), x);
+            p = counted(prob<K>(a.p + (t0 + parent) * a.p_stride * prob_bytes<K>(), x));
+            if (a.q) q = counted(prob<K>(a.q + (t0 + parent) * a.q_stride * prob_bytes<K>(), x));
         } else {
             parent = -1;
         }
