@@ -463,7 +463,9 @@ coli_status coli_latent_plan(coli_serve *serve, const int32_t *q_start, const in
  *         tree_mask ([n_tok x mask_words] 64-bit words) is set: itself and
  *         its ancestors; tokens past the words are not seen.
  * A token that sees nothing gets zeros and lse = -inf.  Cached rows that a
- * token does not see have no part in its result, whatever they hold.
+ * token does not see have no part in its result, whatever they hold; of those
+ * it sees, a latent value that is not finite makes that output NaN, and all
+ * outputs where its score is not -inf.
  * COLI_E_STATE before the first plan.  Pointers 16-byte aligned, strides multiples
  * of 8 elements. */
 coli_status coli_latent_decode(coli_serve *serve, const void *q_lat, int64_t ql_tok_stride, int64_t ql_head_stride,

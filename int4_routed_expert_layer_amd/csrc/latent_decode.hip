@@ -99,13 +99,13 @@ struct Shared {
     __device__ float *maxima(int t, int half) const { return red + ((t & 1) * 2 + half) * kTileRows; }
 };
 
-// In the careful pass, rows that a step hides from some are cleaned: they
-// hold what other branches left there, their weight is zero, and zero times
-// inf or NaN must not reach a row that does not see them.  (A row that sees
-// such a key has a NaN score.)
+// In the careful pass, values that are not finite are taken as zero in the steps
+// that hide keys from some row: such keys hold what other branches left there,
+// their weight is zero, and zero times inf or NaN must not reach a row that does
+// not see them.  spoil_seen() then sees to the rows that do.
 template <bool BF>
 __device__ __forceinline__ void clean(const Shared &sh, int t) {
-    dev::lds_barrier();                                  // no copy is in flight, and every wave has read the step's keys
+    dev::lds_barrier();                                  // every wave has read the step's keys; the copies in flight are of other steps
     u32x4 *v = reinterpret_cast<u32x4 *>(sh.ring(t));
     for (int i = threadIdx.x; i < kLatentBlocks * kBlockBytes / 16; i += kThreads) {
         u32x4 w = v[i];
@@ -430,6 +430,65 @@ __device__ __forceinline__ void sum_item(const DecodeArgs &a, const DecodeItem &
     if (__any(z != 0.0f)) *sh.bad = 1;
 }
 
+// After the careful pass: outputs whose value is not finite in a key that their row
+// sees, in the steps that were cleaned, become NaN, as they do by themselves in
+// the other steps.  (An infinite latent is part of the key too: the row's score is
+// then NaN or +inf and the whole row NaN, or it is -inf and the output 0 * inf.)
+// The keys are read from the cache again, eight at a time: this is rare, and a count
+// of them beside the products, in the registers that those leave, spills 673.
+template <bool BF>
+__device__ __forceinline__ void spoil_seen(const DecodeArgs &a, const DecodeItem &it, const Shared &sh, int rows, f32x16 (&acc)[4][2]) {
+    const int lane = threadIdx.x & 63, wave = dev::wave_id() & 3, l31 = lane & 31, lh = lane >> 5;
+    const int32_t *table = a.cache.table + it.seq * a.cache.table_stride;
+    const int shift = a.cache.page_shift, cols = a.cache.table_cols;
+    const int node0 = (it.row0 + min(l31, rows - 1)) / a.n_heads, node1 = (it.row0 + min(32 + l31, rows - 1)) / a.n_heads;
+    constexpr int kBatch = 8;
+    uint64_t even[2] = {0, 0}, odd[2] = {0, 0};          // of the lane's two rows: columns 128 wave + 2 bit (and + 1) to spoil
+#pragma unroll 1
+    for (int key = max(sh.t0, max(sh.open, 0) / kStepKeys) * kStepKeys; key < min(sh.t1 * kStepKeys, it.len); key += kBatch) {
+        uint32_t off[kBatch], any = 0;                   // of values 128 wave + 2 lane and the next
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            const int pos = min(key + j, it.len - 1), at = pos >> shift;
+            int page = dev::ld_uniform(table + min(at, max(cols, 1) - 1));
+            if (page < 0 || page >= a.cache.n_pages || at >= cols) page = 0;   // flagged where it was copied
+            const uint8_t *row = a.cache.base + (page * a.cache.page_stride + static_cast<int64_t>(pos & ((1 << shift) - 1)) * kCacheRow) * 2;
+            off[j] = *reinterpret_cast<const uint32_t *>(row + 256 * wave + 4 * lane);
+        }
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            off[j] = dev::nonfinite_halves<BF>(off[j]);
+            any |= off[j];
+        }
+        if (!__any(any != 0)) continue;
+        const uint64_t seen0 = seen_keys(a, it, node0, key), seen1 = seen_keys(a, it, node1, key);   // none past the last key
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            const uint64_t e = __ballot(off[j] & 0xFFFFu), o = __ballot(off[j] >> 16);
+            if ((seen0 >> j) & 1) {
+                even[0] |= e;
+                odd[0] |= o;
+            }
+            if ((seen1 >> j) & 1) {
+                even[1] |= e;
+                odd[1] |= o;
+            }
+        }
+    }
+#pragma unroll
+    for (int rb = 0; rb < 2; ++rb) {
+        even[rb] >>= 2 * lh;
+        odd[rb] >>= 2 * lh;
+#pragma unroll
+        for (int cb = 0; cb < 4; ++cb)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {               // column 32 cb + 8 (i / 4) + 4 lh + i % 4
+                const uint32_t here = static_cast<uint32_t>((i & 1 ? odd[rb] : even[rb]) >> (16 * cb + 4 * (i >> 2) + ((i & 3) >> 1))) & 1u;
+                acc[cb][rb][i] += __uint_as_float(-here & 0x7FC00000u);   // NaN or nothing, without 128 conditions held at once
+            }
+    }
+}
+
 // This workgroup's item of a round (no item: n == 0) and its steps.
 __device__ __forceinline__ DecodeItem take_item(const DecodeArgs &a, int round, bool &more, Shared &sh) {
     typedef int32_t int8v __attribute__((ext_vector_type(8)));
@@ -497,6 +556,7 @@ __global__ __launch_bounds__(kThreads, 2) void latent_decode_kernel(DecodeArgs a
             for (int careful = 0; careful < 2; ++careful) {
                 dev::lds_barrier();
                 sum_item<BF, ONCE>(a, it, sh, kv_lds, careful, bad_page, acc);
+                if (careful) spoil_seen<BF>(a, it, sh, rows, acc);
                 dev::lds_barrier();
                 if (!(s_bad && sh.t1 * kStepKeys > sh.open)) break;
             }

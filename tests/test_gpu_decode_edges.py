@@ -1,0 +1,48 @@
+"""Absorbed latent attention (Serve.decode): keys of infinite latents wherever
+they lie."""
+import numpy as np
+import pytest
+
+import serve_case as R
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+if not torch.cuda.is_available():
+    pytest.skip("no GPU", allow_module_level=True)
+
+from test_gpu_latent_decode import Case  # noqa: E402
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("tree", [False, True])
+@pytest.mark.parametrize("length,page", [(92, 16), (733, 1)])
+@pytest.mark.parametrize("back", [82, 22, 5, 2, 1])
+@pytest.mark.parametrize("value", [float("inf"), float("-inf")])
+def test_an_infinite_latent_that_a_row_sees(back, length, page, value, tree, dtype):
+    """Column 9 of one cached row is infinite, in the context or in one of the
+    five last positions, of one piece or of many.  A row that sees it with a query of the same sign has a
+    score of +inf and is NaN; with the other sign the score is -inf, so the
+    weight is zero and the column 0 * inf, NaN, while the rest is as if the key
+    were not there.  A row that does not see it is as if it were not there."""
+    heads, n, pos = 20, 5, length - back
+    sets = [R.ancestors([-1, 0, 0, 1, 2])] if tree else None
+    c = Case([length], [n], heads, page, dtype, sets=sets, seed=31)
+    side = torch.where(torch.arange(heads) % 2 == 0, 1.0, -1.0)
+    c.q[:, :, 9] = (side[None] * (0.5 + c.q[:, :, 9].float().abs())).to(c.q.dtype)
+    c.cache[c.table[0, pos // page], pos % page, 9] = value
+    out, lse = (x.double().cpu().numpy() for x in c.run())
+    see, kv = c.seen(0), c.kv[0].double().numpy()
+    others = np.arange(R.LATENT) != 9
+    for h in range(heads):
+        sees = see.copy()
+        sees[:, pos] = False
+        o, e, bo, be = R.attend(c.q[:, h].double().numpy(), kv, kv[:, :R.LATENT], sees, c.scale, dtype)
+        for i in range(n):
+            if not see[i, pos]:
+                assert np.all(np.abs(out[i, h] - o[i]) <= bo[i]) and abs(lse[i, h] - e[i]) <= be[i], (i, h)
+            elif side[h] * value > 0:
+                assert np.isnan(out[i, h]).all() and np.isnan(lse[i, h]), (i, h)
+            else:
+                assert np.isnan(out[i, h, 9]), (i, h)
+                assert np.all(np.abs(out[i, h] - o[i])[others] <= bo[i][others]) and abs(lse[i, h] - e[i]) <= be[i], (i, h)
