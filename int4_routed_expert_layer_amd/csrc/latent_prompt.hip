@@ -328,10 +328,11 @@ __device__ __forceinline__ bool find_tile(const PromptArgs &a, int tiles_cap, in
     tile.head = lin / tiles_cap;
     const int want = tiles_cap - 1 - (lin - tile.head * tiles_cap);
     // Sequence and row tile number `want` of the call: each lane counts one
-    // sequence's tiles.
+    // sequence's tiles.  The scan ends where it finds them, but for the first place,
+    // which looks at the bounds of every sequence.
     int number = 0, nq = 0;
     bool found = false, bad_seq = false;
-    for (int b0 = 0, done = 0; b0 < a.n_seq; b0 += 64) {
+    for (int b0 = 0, done = 0; b0 < a.n_seq && !(found && slot); b0 += 64) {
         const int b = b0 + lane;
         int n = 0, q0 = 0, q1 = 0, k0 = 0, k1 = 0;
         if (b < a.n_seq) {
@@ -339,11 +340,12 @@ __device__ __forceinline__ bool find_tile(const PromptArgs &a, int tiles_cap, in
             q1 = a.q_start[b + 1];
             k0 = a.k_start[b];
             k1 = a.k_start[b + 1];
-            if (q0 >= 0 && q1 >= q0 && q1 <= a.n_q) n = (q1 - q0 + kRows - 1) / kRows;
-            else bad_seq = true;
+            const bool ok = q0 >= 0 && q1 >= q0 && q1 <= a.n_q;
+            if (ok) n = (q1 - q0 + kRows - 1) / kRows;
+            bad_seq = bad_seq || !ok || k0 < 0 || k1 < k0 || k1 > a.n_k;
         }
         const int cum = dev::running_sum(n);
-        const uint64_t hit = __ballot(done + cum > want);
+        const uint64_t hit = found ? 0 : __ballot(done + cum > want);
         if (hit) {
             const int at = __ffsll(static_cast<unsigned long long>(hit)) - 1;
             found = true;
@@ -352,7 +354,6 @@ __device__ __forceinline__ bool find_tile(const PromptArgs &a, int tiles_cap, in
             nq = __builtin_amdgcn_readlane(q1, at) - tile.q0;
             tile.k0 = __builtin_amdgcn_readlane(k0, at);
             tile.nk = __builtin_amdgcn_readlane(k1, at) - tile.k0;
-            break;
         }
         done += __builtin_amdgcn_readlane(cum, 63);
     }
