@@ -449,7 +449,9 @@ coli_status coli_latent_append(coli_serve *serve, const void *c, int64_t c_strid
  * q_start[b] tokens of this step as the last of kv_len[b] cached positions
  * (kv_len may be smaller, even 0: the leading tokens then see nothing).  The plan
  * is made on the device and kept in the handle: every later coli_latent_decode
- * uses it, until the next one.  q_start and kv_len are read by this call alone. */
+ * uses it, until the next one (a decode call that is replayed from a graph after a
+ * plan of another n_tok or n_seq sets bit 0 and does nothing else).  q_start and
+ * kv_len are read by this call alone. */
 coli_status coli_latent_plan(coli_serve *serve, const int32_t *q_start, const int32_t *kv_len, int32_t n_seq, int32_t n_tok,
                              void *stream);
 

@@ -489,13 +489,26 @@ __device__ __forceinline__ void spoil_seen(const DecodeArgs &a, const DecodeItem
     }
 }
 
+typedef int32_t int4v __attribute__((ext_vector_type(4)));
+typedef int32_t int8v __attribute__((ext_vector_type(8)));
+
+// Whether the handle's plan is of this call's numbers of tokens and sequences: not
+// where a call is replayed from a graph after a plan of other sizes, whose items
+// would lie outside its arrays.  Then nothing is done.
+__device__ __forceinline__ bool planned(const DecodeArgs &a, int4v head) { return head[2] == a.n_tok && head[3] == a.n_seq; }
+
 // This workgroup's item of a round (no item: n == 0) and its steps.
 __device__ __forceinline__ DecodeItem take_item(const DecodeArgs &a, int round, bool &more, Shared &sh) {
-    typedef int32_t int8v __attribute__((ext_vector_type(8)));
-    DecodeItem it = __builtin_bit_cast(
-        DecodeItem, dev::ld_uniform(reinterpret_cast<const int8v *>(a.plan.items + static_cast<int64_t>(round) * gridDim.x + blockIdx.x)));
+    const int4v head = dev::ld_uniform(reinterpret_cast<const int4v *>(a.plan.head));
+    const int8v v = dev::ld_uniform(reinterpret_cast<const int8v *>(a.plan.items + static_cast<int64_t>(round) * gridDim.x + blockIdx.x));
+    DecodeItem it = __builtin_bit_cast(DecodeItem, v);
     more = it.seq & kItemMore;
     it.seq &= ~kItemMore;
+    if (__builtin_expect(!planned(a, head), 0)) {
+        dev::flag_if(true, a.err, kErrSeq);
+        it.n = 0;
+        more = false;
+    }
     sh.t0 = 2 * it.t0;
     sh.t1 = min(2 * it.t1, (it.len + kStepKeys - 1) / kStepKeys);
     sh.open = it.len - it.n + (a.mask ? 0 : 1);
@@ -602,7 +615,8 @@ template <bool BF>
 __global__ __launch_bounds__(256) void join_kernel(DecodeArgs a) {
     __shared__ f32x4 s_o[3][4][64];
     __shared__ float s_l[3][64];
-    const int joins = dev::ld_uniform(a.plan.head), most = dev::ld_uniform(a.plan.head + 1);
+    const int4v head = dev::ld_uniform(reinterpret_cast<const int4v *>(a.plan.head));
+    const int joins = planned(a, head) ? head[0] : 0, most = head[1];
     const bool apart = most <= kWavePieces;
     const int per = apart ? kOutBlocks / 4 : kOutBlocks;
     const int lane = threadIdx.x & 63, wave = dev::wave_id();
@@ -695,7 +709,7 @@ __global__ __launch_bounds__(kPlanThreads) void decode_plan_kernel(DecodePlan p,
     // What the first sequences need, nearer than device memory: units, tiles,
     // first item and slot, and first token, tokens, length.
     __shared__ int4 s_seq[kSortMost], s_at[kSortMost];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, of_seq = n_seq;
     int4 *seq = reinterpret_cast<int4 *>(p.seq);         // units, tiles, first item, first slot
     if (tid == 0) {
         s_units = s_work = 0;
@@ -897,6 +911,8 @@ __global__ __launch_bounds__(kPlanThreads) void decode_plan_kernel(DecodePlan p,
     if (tid == 0) {
         p.head[0] = fits ? n_joins : 0;
         p.head[1] = s_most;
+        p.head[2] = n_tok;
+        p.head[3] = of_seq;
     }
     dev::flag_if(bad || !fits, err, kErrSeq);
 }

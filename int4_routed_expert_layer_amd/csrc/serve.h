@@ -35,7 +35,7 @@ struct alignas(16) JoinUnit {
     int32_t out_row, rows, slot0, split;
 };
 struct DecodePlan {
-    int32_t *head;             // [2] join units, the most pieces of one
+    int32_t *head;             // [4] join units, the most pieces of one, tokens, sequences
     DecodeItem *items;
     JoinUnit *joins;
     int32_t *seq;              // [max_seqs x 4] scratch of the planning

@@ -85,7 +85,7 @@ size_t create_bytes(const coli_serve_dims &d, int n_cu) {
     const Sizes z = plan_sizes(d, n_cu);
     return static_cast<size_t>(z.items) * sizeof(DecodeItem) + static_cast<size_t>(z.joins) * sizeof(JoinUnit) +
            static_cast<size_t>(z.slots) * kTileRows * (kLatent + kSlotStats) * sizeof(float) +
-           static_cast<size_t>(z.seqs) * (8 * sizeof(int32_t) + 2 * sizeof(uint64_t) + sizeof(int32_t)) + 4 * sizeof(int32_t);
+           static_cast<size_t>(z.seqs) * (8 * sizeof(int32_t) + 2 * sizeof(uint64_t) + sizeof(int32_t)) + 5 * sizeof(int32_t);
 }
 
 void free_serve(coli_serve *S) {
@@ -174,7 +174,7 @@ coli_status coli_serve_create(const coli_serve_dims *d, int device, coli_serve *
     S->plan.join_cap = static_cast<int>(z.joins);
     S->plan.slot_cap = static_cast<int>(z.slots);
     struct { void **p; size_t n; const char *what; } allocs[] = {
-        {reinterpret_cast<void **>(&S->plan.head), 2 * sizeof(int32_t), "plan head"},
+        {reinterpret_cast<void **>(&S->plan.head), 4 * sizeof(int32_t), "plan head"},
         {reinterpret_cast<void **>(&S->plan.items), z.items * sizeof(DecodeItem), "plan items"},
         {reinterpret_cast<void **>(&S->plan.joins), z.joins * sizeof(JoinUnit), "plan joins"},
         {reinterpret_cast<void **>(&S->plan.seq), z.seqs * 4 * sizeof(int32_t), "plan scratch"},
@@ -194,7 +194,7 @@ coli_status coli_serve_create(const coli_serve_dims *d, int device, coli_serve *
         }
     if ((he = hipMemset(S->best, 0, z.seqs * 2 * sizeof(uint64_t))) != hipSuccess ||
         (he = hipMemset(S->arrived, 0, z.seqs * sizeof(int32_t))) != hipSuccess ||
-        (he = hipMemset(S->plan.head, 0, 2 * sizeof(int32_t))) != hipSuccess ||
+        (he = hipMemset(S->plan.head, 0, 4 * sizeof(int32_t))) != hipSuccess ||
         (he = hipMemset(S->plan.items, 0, z.items * sizeof(DecodeItem))) != hipSuccess ||
         (he = hipMemset(S->err, 0, sizeof(int32_t))) != hipSuccess || (he = hipDeviceSynchronize()) != hipSuccess) {
         fail(nullptr, COLI_E_DEVICE, "handle setup: %s", hipGetErrorString(he));

@@ -1,5 +1,5 @@
 """Absorbed latent attention (Serve.decode): keys of infinite latents wherever
-they lie."""
+they lie, and captured calls whose plan has become another's."""
 import numpy as np
 import pytest
 
@@ -11,7 +11,8 @@ torch = pytest.importorskip("torch")
 if not torch.cuda.is_available():
     pytest.skip("no GPU", allow_module_level=True)
 
-from test_gpu_latent_decode import Case  # noqa: E402
+from test_gpu_latent_decode import DEV, Case  # noqa: E402
+from int4_routed_expert_layer_amd.serve import Serve  # noqa: E402
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
@@ -46,3 +47,36 @@ def test_an_infinite_latent_that_a_row_sees(back, length, page, value, tree, dty
             else:
                 assert np.isnan(out[i, h, 9]), (i, h)
                 assert np.all(np.abs(out[i, h] - o[i])[others] <= bo[i][others]) and abs(lse[i, h] - e[i]) <= be[i], (i, h)
+
+
+@pytest.mark.parametrize("lens,nodes", [([600, 90], [2, 1]), ([40, 40], [1, 1])])
+@pytest.mark.parametrize("more", [([5000, 300], [3, 6]), ([50, 3000, 700], [1, 1, 1])])
+def test_a_captured_call_after_a_larger_plan(lens, nodes, more):
+    """A call captured for few tokens and replayed when the handle holds the plan
+    of a larger step: a flag, and nothing is read or written; with its own plan again, its own result."""
+    c = Case(lens, nodes, 16, 16, seed=41)
+    want, want_lse = c.run()
+    n, T = sum(nodes), sum(more[1])
+    s = Serve(16, T, len(more[0]), 16)
+    q, cache, table = c.q.to(DEV), c.cache.to(DEV), c.table.to(DEV)
+    ql, qp = q[..., :R.LATENT].contiguous(), q[..., R.LATENT:].contiguous()
+    own = c.q_start.to(DEV), torch.tensor(lens, dtype=torch.int32, device=DEV)
+    other = torch.tensor(np.concatenate([[0], np.cumsum(more[1])]), dtype=torch.int32, device=DEV), torch.tensor(more[0], dtype=torch.int32, device=DEV)
+    room, room_lse = torch.empty(T, 16, R.LATENT, dtype=torch.bfloat16, device=DEV), torch.empty(T, 16, device=DEV)
+    out, lse = room[:n], room_lse[:n]
+    s.plan(*own, n_tok=n)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        s.decode(ql, qp, cache, table, c.scale, out=out, lse=lse)
+    for _ in range(2):
+        room.fill_(7.0)
+        room_lse.fill_(7.0)
+        s.plan(*other, n_tok=T)
+        graph.replay()
+        assert s.device_errors() == 1
+        assert torch.all(room == 7.0) and torch.all(room_lse == 7.0)
+        s.plan(*own, n_tok=n)
+        graph.replay()
+        assert s.device_errors() == 0
+        assert torch.equal(out, want) and torch.equal(lse, want_lse)
+    s.close()
