@@ -80,3 +80,10 @@ def test_a_captured_call_after_a_larger_plan(lens, nodes, more):
         assert s.device_errors() == 0
         assert torch.equal(out, want) and torch.equal(lse, want_lse)
     s.close()
+
+
+@pytest.mark.parametrize("lens,nodes,heads", [([5000], [1], 64), ([2000, 17, 900, 1], [2, 1, 3, 1], 33), ([150] * 300, [1] * 300, 16), ([700] * 5, [20] * 5, 64), ([1500], [40], 64)])
+def test_every_row_of_divided_and_many_units(lens, nodes, heads):
+    """All heads of all tokens: each 64-row unit has pieces and a join of its own."""
+    c = Case(lens, nodes, heads, 32, seed=51)
+    c.check(*c.run())
