@@ -1,4 +1,5 @@
-"""Expanded latent attention (Serve.prompt): bounds of sequences past the first 64."""
+"""Expanded latent attention (Serve.prompt): bounds of sequences past the first 64,
+and prompts whose keys are divided into two rounds of parts."""
 import pytest
 
 pytestmark = pytest.mark.gpu
@@ -7,7 +8,7 @@ torch = pytest.importorskip("torch")
 if not torch.cuda.is_available():
     pytest.skip("no GPU", allow_module_level=True)
 
-from test_gpu_latent_prompt import DEV, HEADS  # noqa: E402
+from test_gpu_latent_prompt import DEV, HEADS, Case  # noqa: E402
 from int4_routed_expert_layer_amd.serve import Serve  # noqa: E402
 
 
@@ -34,3 +35,15 @@ def test_bounds_of_any_sequence_set_the_flag(width, n_seq, at, which):
     assert s.device_errors() == 1
     assert torch.equal(out[:at], good[:at])
     s.close()
+
+
+@pytest.mark.parametrize("nq,nk,heads", [([1600], [1600], dict(wide=10, narrow=20)), ([1700], [2500], dict(wide=10, narrow=20)), ([1600, 1690], [1600, 1700], dict(wide=5, narrow=10))])
+@pytest.mark.parametrize("width", ["wide", "narrow"])
+def test_prompts_of_two_rounds_of_parts(width, nq, nk, heads):
+    """At least 768 keys a sequence, fewer than twice the queries, and more than
+    half a round of tiles: the keys are divided though one round would not divide them."""
+    c = Case(nq, nk, heads[width], width, seed=21)
+    out, lse = c.run()
+    c.check(out, lse, heads=[0, heads[width] // 2, heads[width] - 1])
+    again, again_lse = c.run()
+    assert torch.equal(out, again) and torch.equal(lse, again_lse)
