@@ -162,22 +162,6 @@ __device__ __forceinline__ void pipeline_run() {
         pipeline_run<LEFT - READS, MFMAS, READS>();
     }
 }
-// READS reads and MFMAS products in all, with VALU vector instructions of
-// other work after each product.
-template <int LEFT, int READS, int VALU>
-__device__ __forceinline__ void pipeline_mixed_run() {
-    if constexpr (LEFT > 0) {
-        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-        __builtin_amdgcn_sched_group_barrier(0x002, VALU, 0);
-        if constexpr (READS > 0) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-        pipeline_mixed_run<LEFT - 1, READS - 1, VALU>();
-    }
-}
-template <int READS, int MFMAS, int VALU, int AHEAD>
-__device__ __forceinline__ void pipeline_mixed() {
-    __builtin_amdgcn_sched_group_barrier(0x100, AHEAD, 0);
-    pipeline_mixed_run<MFMAS, READS - AHEAD, VALU>();
-}
 template <int READS_ALL, int MFMAS, int READS, int AHEAD>
 __device__ __forceinline__ void pipeline() {
     pipeline_begin<AHEAD>();

@@ -22,9 +22,6 @@
 namespace coli {
 namespace {
 
-using dev::u32x2;
-using dev::u32x4;
-
 constexpr int kSampleThreads = 256, kWalkThreads = 1024;
 // A workgroup takes its slice of a row in chunks of four groups of four elements
 // per thread, all in flight at once; the first of race is loaded before the
