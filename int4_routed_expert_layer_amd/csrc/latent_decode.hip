@@ -29,13 +29,13 @@
 // pieces leave unnormalised sums, maxima and fp32 partial outputs, which
 // join_kernel combines.
 //
-// Measured.  64 tokens of sequences up to 12k, 64 heads, bf16: 66 us and 9 for the
+// Measured.  64 tokens of sequences up to 12k, 64 heads, bf16: 67 us and 10 for the
 // join, 352 MB, 5.3 TB/s in the first: bound by HBM.  Four chains of four tokens up
-// to 128k, 16 heads, f16: 93 and 12 us, 535 MB, 5.8 TB/s.  16 trees of 25 nodes up
+// to 128k, 16 heads, f16: 92 and 13 us, 535 MB, 5.8 TB/s.  16 trees of 25 nodes up
 // to 5k, 64 heads, bf16: 149 us, 960 TFLOP/s against 1223 of a large library
-// product: bound by the matrix units and their clock under load.  One token, 4k,
-// 64 heads: 11 and 5 us, a chain of latencies (the item, its queries, page numbers,
-// keys, four steps, partial results).
+// product; the matrix pipes are busy 43% of the cycles at 2.1 GHz, the product's 70%
+// at 1.5 to 1.9.  One token, 4k, 64 heads: 11.5 and 5.7 us, a chain of latencies (the
+// item, its queries, page numbers, keys, four steps, partial results).
 #include "dev_attn.h"
 
 namespace coli {

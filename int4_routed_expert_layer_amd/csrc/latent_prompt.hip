@@ -23,11 +23,11 @@
 // A call with few tiles divides the keys of each among workgroups that leave
 // unnormalised sums, maxima and fp32 partial outputs; join_parts_kernel adds them.
 //
-// Measured, bf16: 16384 rows, 16 heads: 1.32 ms, 1043 TFLOP/s, against 1223 of a
-// large library product: bound by the matrix units and their clock under
-// load.  4 x 4096 rows, 32 heads: 0.90 ms, 768 TFLOP/s.  Eight prompts of 36..1023
-// rows after 129 keys, 64 heads: 165 us for 353 MB and 85 GFLOP, 70 us each at
-// the card's rates.  There a tile has 18 steps of 2300 clocks (two workgroups at a
+// Measured, bf16: 16384 rows, 16 heads: 1.28 ms, 1073 TFLOP/s, against 1223 of a
+// large library product; the matrix pipes are busy 56% of the cycles at 1.65 GHz,
+// the product's 70% at 1.5 to 1.9.  4 x 4096 rows, 32 heads: 0.76 ms, 908 TFLOP/s,
+// 46% at 1.74.  Eight prompts of 36..1023 rows after 129 keys, 64 heads: 167 us for
+// 353 MB and 85 GFLOP, 70 us each at the card's rates.  There a tile has 18 steps of 2300 clocks (two workgroups at a
 // time; 1280 of them products) and 7 us beside them: finding its place, its
 // queries and first keys from HBM, and its output, of which the other
 // workgroup of the CU hides about half.
@@ -505,8 +505,8 @@ __global__ __launch_bounds__(256, 2) void latent_prompt_kernel(PromptArgs a, int
 // probabilities of step t to LDS, four summing waves with a quarter of the
 // value columns each add step t - 1 for all rows and copy step t + 2.  Each
 // SIMD holds one of either kind.  (One kind of wave, 64-key tiles: 281 spilled
-// registers, 7.8 ms for 4 x 4096 rows, 32 heads, f16; so 1.20 ms, 916 TFLOP/s of
-// 1164 of a large library product, bound by the matrix units.)  A row's scores lie in one wave, which moves
+// registers, 7.8 ms for 4 x 4096 rows, 32 heads, f16; so 1.25 ms, 881 TFLOP/s of
+// 1164 of a large library product, the matrix pipes busy 43% at 1.76 GHz.)  A row's scores lie in one wave, which moves
 // its maximum by itself and leaves the rows' factors for the summing waves.
 constexpr int kSplitThreads = 512;
 
@@ -811,7 +811,7 @@ hipError_t launch_tiles(PromptArgs &a, K kernel, J join, int threads, int blocks
     const int64_t most = (a.n_k + kStepKeys - 1) / kStepKeys / kLeastSteps;
     // Without much context the first tiles see few keys and the last most: two
     // rounds of parts even that out, where they are of 24 steps or more (4096
-    // rows, 12 narrow heads: 127 us in one round, 102 in two; 6 wide heads 114 and 87;
+    // rows, 12 narrow heads: 127 us in one round, 110 in two; 6 wide heads 114 and 84;
     // but 1024 rows, 32 narrow heads: 34 and 39).
     const int64_t even = a.causal && a.n_k < 2ll * a.n_q ? std::min<int64_t>(2 * places, a.part_cap) / tiles : 0;
     const int64_t want = std::max<int64_t>(std::min(places, a.part_cap) / tiles, std::min<int64_t>(even, a.n_k / a.n_seq / (24 * kStepKeys)));
