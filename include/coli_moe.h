@@ -377,6 +377,19 @@ coli_status coli_probe_read(const void *buf, size_t bytes, uint32_t *sink, void 
  *   coli_latent_prompt  expanded attention of whole prompts.
  *   coli_draft_verify   accepts drafted tokens and samples the next one.
  *   coli_latent_keep    moves the accepted nodes' rows together.
+ *   coli_latent_read    gathers cached rows, one sequence behind the other.
+ *   coli_latent_plan_shared  a plan for groups of sequences that share a prefix.
+ *   coli_beam_select    the best continuations of a group's beams.
+ *   coli_beam_reorder   the cache and block tables of the beams that go on.
+ *
+ * A cache may also hold its rows in 8 bits (coli_latent8_append, _decode and
+ * _keep, and COLI_CACHE_8 where a call takes the kind): a row is then 656 bytes,
+ *   bytes 0..511    the latent values in e4m3 (OCP: 4 exponent bits, bias 7, 3
+ *                   fraction bits, largest 448, no infinities),
+ *   bytes 512..639  the 64 rotary values in the handle's 16-bit type,
+ *   bytes 640..655  for each 32 latent values a scale 2^(byte - 127),
+ * and stands for e4m3 value * scale.  Strides of such a cache count bytes; cache
+ * and strides are multiples of 16.
  *
  * The tokens of a call are those of its sequences one after the other: the
  * tokens of sequence b are q_start[b] .. q_start[b + 1] - 1 (int32
@@ -388,6 +401,7 @@ coli_status coli_probe_read(const void *buf, size_t bytes, uint32_t *sink, void 
  * outputs of the sequences concerned are unspecified.  Calls on one handle
  * share its plan and scratch and must not overlap in time. */
 typedef enum { COLI_HALF_BF16 = 0, COLI_HALF_F16 = 1 } coli_half;
+typedef enum { COLI_CACHE_16 = 0, COLI_CACHE_8 = 1 } coli_cache_kind;
 typedef enum { COLI_PROB_F32 = 0, COLI_PROB_BF16 = 1, COLI_PROB_F16 = 2 } coli_prob;
 
 typedef struct {
@@ -529,6 +543,90 @@ coli_status coli_latent_keep(coli_serve *serve, void *cache, int64_t page_stride
                              int64_t layer_stride, const int32_t *block_table, int64_t table_stride, int32_t table_cols,
                              const int32_t *q_start, const int32_t *kv_len, int32_t n_seq, int32_t n_tok, const int32_t *path,
                              int64_t path_stride, int32_t path_cols, void *stream);
+
+/* The same over a cache of 8-bit rows.
+ *
+ * Append: each latent value is computed in fp32 and rounded once, to the nearest
+ * multiple of its group's scale (ties to even) that e4m3 holds.  The scale is the
+ * least power of two that brings the group's largest value to 448 or below, no less
+ * than 2^-110 (bf16) or 2^-15 (f16), so that every stored value is exactly one of the
+ * 16-bit type; at its greatest, 2^120 or 2^8, values end at 240 times it.  A value that
+ * is not finite in the 16-bit type is stored as NaN and has no part in the scale.
+ * Decode computes with the values that the rows stand for, as coli_latent_decode does
+ * with those of a 16-bit cache. */
+coli_status coli_latent8_append(coli_serve *serve, const void *c, int64_t c_stride, const void *norm_weight, float eps,
+                                const float *cos_table, const float *sin_table, int32_t n_positions, int32_t interleaved,
+                                const int32_t *positions, const int64_t *slots, int32_t n_tok, void *cache, int64_t page_stride,
+                                int32_t n_pages, const void *q_pe, int64_t q_tok_stride, int64_t q_head_stride, void *q_out,
+                                void *stream);
+coli_status coli_latent8_decode(coli_serve *serve, const void *q_lat, int64_t ql_tok_stride, int64_t ql_head_stride,
+                                const void *q_pe, int64_t qp_tok_stride, int64_t qp_head_stride, const void *cache,
+                                int64_t page_stride, int32_t n_pages, const int32_t *block_table, int64_t table_stride,
+                                int32_t table_cols, const uint64_t *tree_mask, int32_t mask_words, float scale, int32_t n_tok,
+                                void *out, float *lse, void *stream);
+coli_status coli_latent8_keep(coli_serve *serve, void *cache, int64_t page_stride, int32_t n_pages, int32_t n_layers,
+                              int64_t layer_stride, const int32_t *block_table, int64_t table_stride, int32_t table_cols,
+                              const int32_t *q_start, const int32_t *kv_len, int32_t n_seq, int32_t n_tok, const int32_t *path,
+                              int64_t path_stride, int32_t path_cols, void *stream);
+
+/* Read cached rows back as 16-bit values: row k_start[b] + i of out ([n_rows x 576],
+ * row stride out_stride, 16-byte aligned, a multiple of 8) becomes position first[b] +
+ * i of sequence b, for the k_start[b + 1] - k_start[b] rows of it (int32 [n_seq +
+ * 1], ascending, within 0..n_rows; first NULL: positions from 0).  The bits of a 16-bit
+ * cache's row, or the values of an 8-bit one's, exactly.  Rows of out that no sequence
+ * covers are left as they are.  coli_latent_prompt's keys begin with such rows. */
+coli_status coli_latent_read(coli_serve *serve, int32_t cache_kind, const void *cache, int64_t page_stride, int32_t n_pages,
+                             const int32_t *block_table, int64_t table_stride, int32_t table_cols, const int32_t *first,
+                             const int32_t *k_start, int32_t n_seq, int32_t n_rows, void *out, int64_t out_stride, void *stream);
+
+/* Plan a step whose sequences come in groups that begin with the same tokens: group g
+ * is sequences group_start[g] .. group_start[g + 1] - 1 (int32 [n_groups + 1],
+ * ascending, within 0..n_seq; sequences of no group are planned as before), of which
+ * the first prefix_len[g] positions hold the same rows (on the same pages, or copies of
+ * them; the call trusts that, and reads them through one sequence's row of the block
+ * table).  The decode calls that follow give what they give after coli_latent_plan, up to
+ * the rounding of their sums, and attend to a group's prefix once for all its
+ * tokens: to those of its positions that every token of the group sees as context, in
+ * whole tiles of 64.  Where the pieces of all sequences and groups would exceed the
+ * handle's room (more than four per CU) nothing is shared.  Groups that do not
+ * ascend set bit 0 and nothing is shared. */
+coli_status coli_latent_plan_shared(coli_serve *serve, const int32_t *q_start, const int32_t *kv_len, int32_t n_seq, int32_t n_tok,
+                                    const int32_t *group_start, const int32_t *prefix_len, int32_t n_groups, void *stream);
+
+/* Select the best continuations of beams.  Row g * beams + b of logits ([n_groups *
+ * beams x vocab] of `kind`, row stride logits_stride) holds the logits z behind beam b
+ * of group g, scores[g * beams + b] (fp32) its score.  The score of token x behind b is
+ * score_b + z_x - log sum_y exp z_y.  Outputs [n_groups x keep]: the keep best over all
+ * beams and tokens, from the best down, equal ones in the order of beams and then
+ * tokens: their scores (fp32), beams and tokens (int32).  A beam whose score is not
+ * finite has no continuation, nor has a token whose logit is -inf or NaN (it counts as
+ * -inf); where a group has fewer than keep, the rest is -inf, -1 and -1.  A row of a
+ * live beam with an infinite logit, or with none above -inf, has no continuation and sets
+ * bit 3.  Scores are compared in 64 bits, with the logarithm from a sum of fp32
+ * exponentials.  beams and keep up to 64, vocab up to 2^20 (COLI_E_UNSUPPORTED beyond),
+ * n_groups * beams up to max_seqs.  The call uses the partial results' room. */
+coli_status coli_beam_select(coli_serve *serve, const void *logits, int64_t logits_stride, int32_t kind, int32_t vocab,
+                             const float *scores, int32_t n_groups, int32_t beams, int32_t keep, float *out_scores,
+                             int32_t *out_parents, int32_t *out_tokens, void *stream);
+
+/* Reorder the beams of a paged cache: place j of group g goes on as beam p =
+ * parents[g * beams + j] (0..beams - 1) of it.  The beams of a group have one length,
+ * kv_len[g * beams + j], and share pages before their last one at most: the page of
+ * position kv_len, if any, and those behind it are each beam's own.  out_table (int32
+ * [n_groups * beams x table_cols], not overlapping block_table) gets the places' block
+ * tables: p's pages before that of position kv_len, and from there on the own pages of
+ * one old beam each: p's for the first place that continues p, for any other those of a
+ * beam that no place continues, in ascending order.  To these the rows of p's last page
+ * are copied, in each of n_layers caches (layer_stride apart).  A parent of -1: the
+ * place takes a beam that is left over as it is.  (So one call also forks a prompt: its
+ * pages are beam 0's, the others' tables hold own pages from that of kv_len on, and all
+ * parents are 0.)  Other parents out of range count as -1 and set bit 2; a group
+ * of unequal lengths sets bit 0 and stays as it is; where a copy's page is out of range
+ * bit 1 is set and nothing copied. */
+coli_status coli_beam_reorder(coli_serve *serve, int32_t cache_kind, void *cache, int64_t page_stride, int32_t n_pages,
+                              int32_t n_layers, int64_t layer_stride, const int32_t *block_table, int64_t table_stride,
+                              int32_t table_cols, const int32_t *kv_len, const int32_t *parents, int32_t n_groups, int32_t beams,
+                              int32_t *out_table, int64_t out_stride, void *stream);
 
 #ifdef __cplusplus
 }

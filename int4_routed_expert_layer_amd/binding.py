@@ -64,6 +64,15 @@ SIGNATURES = {
     "coli_draft_verify": (C.c_int, [_p, _p, _i64, _p, _i64, _i32, _i32, _p, _p, _p, _i32, _i32, _p, _p, _i64, _p, _i32, _p, _p,
                                     _p]),
     "coli_latent_keep": (C.c_int, [_p, _p, _i64, _i32, _i32, _i64, _p, _i64, _i32, _p, _p, _i32, _i32, _p, _i64, _i32, _p]),
+    "coli_latent8_append": (C.c_int, [_p, _p, _i64, _p, _f, _p, _p, _i32, _i32, _p, _p, _i32, _p, _i64, _i32, _p, _i64, _i64,
+                                      _p, _p]),
+    "coli_latent8_decode": (C.c_int, [_p, _p, _i64, _i64, _p, _i64, _i64, _p, _i64, _i32, _p, _i64, _i32, _p, _i32, _f, _i32,
+                                      _p, _p, _p]),
+    "coli_latent8_keep": (C.c_int, [_p, _p, _i64, _i32, _i32, _i64, _p, _i64, _i32, _p, _p, _i32, _i32, _p, _i64, _i32, _p]),
+    "coli_latent_read": (C.c_int, [_p, _i32, _p, _i64, _i32, _p, _i64, _i32, _p, _p, _i32, _i32, _p, _i64, _p]),
+    "coli_latent_plan_shared": (C.c_int, [_p, _p, _p, _i32, _i32, _p, _p, _i32, _p]),
+    "coli_beam_select": (C.c_int, [_p, _p, _i64, _i32, _i32, _p, _i32, _i32, _i32, _p, _p, _p, _p]),
+    "coli_beam_reorder": (C.c_int, [_p, _i32, _p, _i64, _i32, _i32, _i64, _p, _i64, _i32, _p, _p, _i32, _i32, _p, _i64, _p]),
 }
 KERNEL_KINDS = ["router", "topk", "union", "plan", "gateup", "down", "combine"]
 

@@ -71,6 +71,14 @@ __device__ __forceinline__ uint32_t nonfinite_halves(uint32_t w) {
     return c * 0xFFFFu;
 }
 
+// The lower or upper two of a dword's four e4m3 values times the scale's power of two
+// (a float whose exponent bits are the scale's byte), as 16-bit values.
+template <bool BF, bool UPPER>
+__device__ __forceinline__ uint32_t of_fp8(uint32_t w, float by) {
+    if constexpr (BF) return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, by, UPPER));
+    else return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, by, UPPER));
+}
+
 // LDS tiles hold rows of 128 bytes (64 values), the rows of one 64-column block
 // after each other.  The 16-byte unit q of row r lies at unit q ^ ((r >> 1) & 7).
 // Measured with eight waves reading, this is free of conflicts (4.6 clocks per

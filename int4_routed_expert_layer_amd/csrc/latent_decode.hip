@@ -49,8 +49,13 @@ using dev::u32x4;
 constexpr int kStepKeys = 32;
 constexpr int kBlocks = kCacheRow / 64;                  // 64-column blocks of a cached row: 8 latent, 1 rotary
 constexpr int kLatentBlocks = kLatent / 64;
-constexpr int kBlockBytes = kStepKeys * 128;
-constexpr int kStepBytes = kBlocks * kBlockBytes;        // 36 KB
+// Distance of a step's blocks in LDS.  Values of an 8-bit cache are written there by
+// the waves, 32 lanes to a key: 16 bytes between the blocks put a write's units, which
+// lie in eight of them, on different banks.
+template <bool Q8>
+constexpr int kBlockBytes = kStepKeys * 128 + (Q8 ? 16 : 0);
+template <bool Q8>
+constexpr int kStepBytes = kBlocks * kBlockBytes<Q8>;    // 36 KB
 constexpr int kRing = 4;
 constexpr int kDepth = kCacheRow / 32;                   // K steps of the first product
 // The running maximum of a row moves only when a step exceeds it by more than
@@ -94,7 +99,8 @@ struct Shared {
     float *red, *fac, *sum;            // [2][2][64] maxima by step parity and key half; [64]; [2][64]
     int *raise, *bad;                  // [3] by step; one flag
     int t0, t1, open;                  // steps; keys below `open` are seen by every row
-    __device__ uint8_t *ring(int t) const { return kv + ((t - t0) & (kRing - 1)) * kStepBytes; }
+    template <bool Q8>
+    __device__ uint8_t *ring(int t) const { return kv + ((t - t0) & (kRing - 1)) * kStepBytes<Q8>; }
     __device__ uint8_t *weights(int t) const { return p + (t & 1) * (kTileRows * 64); }
     __device__ float *maxima(int t, int half) const { return red + ((t & 1) * 2 + half) * kTileRows; }
 };
@@ -103,11 +109,11 @@ struct Shared {
 // that hide keys from some row: such keys hold what other branches left there,
 // their weight is zero, and zero times inf or NaN must not reach a row that does
 // not see them.  spoil_seen() then sees to the rows that do.
-template <bool BF>
+template <bool BF, bool Q8>
 __device__ __forceinline__ void clean(const Shared &sh, int t) {
     dev::lds_barrier();                                  // every wave has read the step's keys; the copies in flight are of other steps
-    u32x4 *v = reinterpret_cast<u32x4 *>(sh.ring(t));
-    for (int i = threadIdx.x; i < kLatentBlocks * kBlockBytes / 16; i += kThreads) {
+    u32x4 *v = reinterpret_cast<u32x4 *>(sh.ring<Q8>(t));
+    for (int i = threadIdx.x; i < kLatentBlocks * kBlockBytes<Q8> / 16; i += kThreads) {
         u32x4 w = v[i];
 #pragma unroll
         for (int d = 0; d < 4; ++d) w[d] &= ~dev::nonfinite_halves<BF>(w[d]);
@@ -116,18 +122,99 @@ __device__ __forceinline__ void clean(const Shared &sh, int t) {
     dev::lds_barrier();
 }
 
+// A wave's share of the steps of an 8-bit cache: of each step keys 4 wave .. + 3, loaded
+// two steps before they are written to LDS as the 16-bit values that they stand for,
+// so that the products are those of a 16-bit cache.  (Every stored value is one of
+// the 16-bit type: the scales are powers of two within its range.)  Lane L holds 16
+// values of keys L / 32 and 2 + L / 32 from value 16 (L % 32) on, their scales, and of
+// the lower 32 lanes each 8 rotary values of key L / 8.
+struct Stage {
+    u32x4 q[2], pe;
+    uint32_t by[2];
+};
+template <bool BF, bool ONCE>
+struct Source8 {
+    const uint8_t *base;
+    const int32_t *table;
+    int64_t page_bytes;
+    int shift, cols, n_pages, len, last, key0;
+    bool bad = false;
+    int page;                          // of the step that is loaded next, where it is the wave's
+
+    __device__ __forceinline__ Source8(const DecodeArgs &a, const DecodeItem &it, const Shared &sh)
+        : base(a.cache.base), table(a.cache.table + it.seq * a.cache.table_stride), page_bytes(a.cache.page_bytes), shift(a.cache.page_shift),
+          cols(a.cache.table_cols), n_pages(a.cache.n_pages), len(it.len), last(sh.t1 - 1), key0(4 * dev::wave_id()) {}
+    // Pages of four rows or more hold all of a wave's keys of a step: the number is then
+    // read by the scalar unit, a step ahead.
+    __device__ __forceinline__ void ask(int t) {
+        const int pos = min(min(t, last) * kStepKeys + key0, len - 1);
+        page = dev::ld_uniform(table + min(pos >> shift, max(cols, 1) - 1));
+    }
+    __device__ __forceinline__ const uint8_t *row(int t, int k) {
+        const int pos = min(min(t, last) * kStepKeys + key0 + k, len - 1), at = pos >> shift;
+        int p = shift >= 2 ? page : table[min(at, max(cols, 1) - 1)];
+        if (p < 0 || p >= n_pages || at >= cols) {
+            bad = true;
+            p = 0;
+        }
+        return base + p * page_bytes + (pos & ((1 << shift) - 1)) * kRow8Bytes;
+    }
+    static __device__ __forceinline__ u32x4 load16(const uint8_t *p) {
+        const __attribute__((address_space(1))) u32x4 *g = (const __attribute__((address_space(1))) u32x4 *)p;
+        if constexpr (ONCE) return __builtin_nontemporal_load(g);
+        else return *g;
+    }
+    __device__ __forceinline__ void load(Stage &s, int t) {
+        const int lane = threadIdx.x & 63, c = lane & 31;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const uint8_t *r = row(t, 2 * j + (lane >> 5));
+            s.q[j] = load16(r + 16 * c);
+            s.by[j] = *(const __attribute__((address_space(1))) uint8_t *)(r + kRow8Scales + (c >> 1));
+        }
+        if (lane < 32) s.pe = load16(row(t, lane >> 3) + kRow8Rope + 16 * (lane & 7));
+        ask(t + 1);
+    }
+    __device__ __forceinline__ void store_latent(const Stage &s, uint8_t *place, int j) const {
+        const int lane = threadIdx.x & 63, c = lane & 31, r = key0 + 2 * j + (lane >> 5);
+        const float by = __uint_as_float(s.by[j] << 23);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            *reinterpret_cast<u32x4 *>(place + (c >> 2) * kBlockBytes<true> + dev::tile_unit(r, 2 * (c & 3) + i)) =
+                u32x4{dev::of_fp8<BF, false>(s.q[j][2 * i], by), dev::of_fp8<BF, true>(s.q[j][2 * i], by),
+                      dev::of_fp8<BF, false>(s.q[j][2 * i + 1], by), dev::of_fp8<BF, true>(s.q[j][2 * i + 1], by)};
+    }
+    __device__ __forceinline__ void store_rope(const Stage &s, uint8_t *place) const {
+        const int lane = threadIdx.x & 63;
+        if (lane < 32) *reinterpret_cast<u32x4 *>(place + kLatentBlocks * kBlockBytes<true> + dev::tile_unit(key0 + (lane >> 3), lane & 7)) = s.pe;
+    }
+    __device__ __forceinline__ void store(const Stage &s, uint8_t *place) const {
+        store_latent(s, place, 0);
+        store_latent(s, place, 1);
+        store_rope(s, place);
+    }
+};
+
 // The scoring waves' part of an item: wave (wm, wk) scores keys 16 wk .. + 15 of
 // each step for rows 32 wm .. + 31; lane L owns rows row and row + 16, row =
 // 32 wm + L % 16.  Leaves the running maxima in m.
-template <bool BF>
+template <bool BF, bool ONCE, bool Q8>
 __device__ __forceinline__ void score_item(const DecodeArgs &a, const DecodeItem &it, const Shared &sh, int rows, bool careful,
-                                           float (&m)[2]) {
+                                           bool &bad_page, float (&m)[2]) {
     const int lane = threadIdx.x & 63, wave = dev::wave_id();
     const int wm = wave & 1, wk = (wave >> 1) & 1, l15 = lane & 15, lq = lane >> 4;
     const int row = 32 * wm + l15;
     const float c = a.scale * kLog2e;
     int node[2];
     u32x4 q[kDepth][2];
+    Stage st[2];                                         // of an 8-bit cache: steps t0 and t0 + 1, later t + 1 and t + 2
+    Source8<BF, ONCE> src(a, it, sh);
+    if constexpr (Q8)
+        if (sh.t0 < sh.t1) {
+            src.ask(sh.t0);
+            src.load(st[0], sh.t0);
+            src.load(st[1], sh.t0 + 1);
+        }
 #pragma unroll
     for (int rb = 0; rb < 2; ++rb) node[rb] = (it.row0 + min(row + 16 * rb, rows - 1)) / a.n_heads;
     if (sh.t0 < sh.t1) {
@@ -136,7 +223,7 @@ __device__ __forceinline__ void score_item(const DecodeArgs &a, const DecodeItem
         // its products take them, they let the first step begin 11400 clocks after
         // the item, so 3900 (one token, 4096 keys 19.9 -> 16.9 us).
         const int r = 8 * wave + (lane >> 3), unit = ((lane & 7) ^ dev::tile_swz(r)) << 4;
-        const uint32_t at = dev::lds_address(sh.kv) + 2 * kStepBytes + wave * 1024;
+        const uint32_t at = dev::lds_address(sh.kv) + 2 * kStepBytes<Q8> + wave * 1024;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const int rr = it.row0 + min(r + 32 * h, rows - 1), n = rr / a.n_heads, head = rr - n * a.n_heads;
@@ -145,15 +232,15 @@ __device__ __forceinline__ void score_item(const DecodeArgs &a, const DecodeItem
             const uint8_t *qp = a.q_pe + (tok * a.qp_tok + head * a.qp_head) * 2 + unit;
 #pragma unroll
             for (int b = 0; b < kBlocks; ++b)
-                dev::copy16_to_lds_free(b < kLatentBlocks ? ql + 128 * b : qp, at + h * kStepBytes + b * kBlockBytes);
+                dev::copy16_to_lds_free(b < kLatentBlocks ? ql + 128 * b : qp, at + h * kStepBytes<Q8> + b * kBlockBytes<Q8>);
         }
         dev::copy_barrier();
-        const uint8_t *mine = sh.kv + (2 + wm) * kStepBytes;
+        const uint8_t *mine = sh.kv + (2 + wm) * kStepBytes<Q8>;
 #pragma unroll
         for (int k = 0; k < kDepth; ++k)
 #pragma unroll
             for (int rb = 0; rb < 2; ++rb)
-                q[k][rb] = *reinterpret_cast<const u32x4 *>(mine + (k >> 1) * kBlockBytes + dev::tile_unit(l15 + 16 * rb, 4 * (k & 1) + lq));
+                q[k][rb] = *reinterpret_cast<const u32x4 *>(mine + (k >> 1) * kBlockBytes<Q8> + dev::tile_unit(l15 + 16 * rb, 4 * (k & 1) + lq));
     }
     __builtin_amdgcn_s_setprio(2);   // the step waits for these waves: the summing ones fill what they leave
     m[0] = m[1] = -__builtin_inff();
@@ -161,9 +248,9 @@ __device__ __forceinline__ void score_item(const DecodeArgs &a, const DecodeItem
     f32x4 s[2], s_prev[2];
     float sum_prev[2];
     auto score = [&](int t) {
-        const uint8_t *kr = sh.ring(t) + 16 * wk * 128;
+        const uint8_t *kr = sh.ring<Q8>(t) + 16 * wk * 128;
         auto key = [&](int k) {
-            return *reinterpret_cast<const u32x4 *>(kr + (k >> 1) * kBlockBytes + dev::tile_unit(l15, 4 * (k & 1) + lq));
+            return *reinterpret_cast<const u32x4 *>(kr + (k >> 1) * kBlockBytes<Q8> + dev::tile_unit(l15, 4 * (k & 1) + lq));
         };
         u32x4 kf[kKeyAhead];
 #pragma unroll
@@ -247,20 +334,27 @@ __device__ __forceinline__ void score_item(const DecodeArgs &a, const DecodeItem
         }
         l[0] += sum_prev[0];
         l[1] += sum_prev[1];
-        if (careful && (t + 1) * kStepKeys > sh.open) clean<BF>(sh, t);
+        if (careful && (t + 1) * kStepKeys > sh.open) clean<BF, Q8>(sh, t);
+    };
+    // Step t + 1 of an 8-bit cache into LDS; its place is asked for step t + 3.
+    auto pass_on = [&](Stage &from, int t) {
+        src.store(from, sh.ring<Q8>(t + 1));
+        src.load(from, t + 3);
     };
 
     if (sh.t0 < sh.t1) {
         // First step: its maxima are exchanged before it is weighed.
+        if constexpr (Q8) pass_on(st[0], sh.t0 - 1);
         dev::lds_barrier();
         score(sh.t0);
         post_max(sh.t0, s);
+        if constexpr (Q8) pass_on(st[1], sh.t0);
         dev::lds_barrier();
         take_max(sh.t0, 0.0f);
         weigh(sh.t0, s, sum_prev);
         s_prev[0] = s[0];
         s_prev[1] = s[1];
-        for (int t = sh.t0 + 1; t < sh.t1; ++t) {
+        auto step = [&](int t, Stage &from) {
             dev::lds_barrier();
             const int raise = sh.raise[(t - 1 - sh.t0) % 3];
             if (threadIdx.x == 0) sh.raise[(t + 1 - sh.t0) % 3] = 0;
@@ -270,6 +364,17 @@ __device__ __forceinline__ void score_item(const DecodeArgs &a, const DecodeItem
             if (__any(lane_max(s[0]) > limit[0] || lane_max(s[1]) > limit[1])) sh.raise[(t - sh.t0) % 3] = 1;
             s_prev[0] = s[0];
             s_prev[1] = s[1];
+            if constexpr (Q8) pass_on(from, t);
+        };
+        if constexpr (Q8) {                              // two steps a turn: what is in flight stays in its registers
+            int t = sh.t0 + 1;
+            for (; t + 1 < sh.t1; t += 2) {
+                step(t, st[0]);
+                step(t + 1, st[1]);
+            }
+            if (t < sh.t1) step(t, st[0]);
+        } else {
+            for (int t = sh.t0 + 1; t < sh.t1; ++t) step(t, st[0]);
         }
         dev::lds_barrier();
         settle(sh.t1 - 1, sh.raise[(sh.t1 - 1 - sh.t0) % 3]);
@@ -279,11 +384,12 @@ __device__ __forceinline__ void score_item(const DecodeArgs &a, const DecodeItem
         const float sum = dev::sum_halves(dev::sum_quarters(l[rb]));
         if (lq == 0) sh.sum[wk * kTileRows + row + 16 * rb] = sum;
     }
+    if constexpr (Q8) bad_page = bad_page || src.bad;
 }
 
 // The summing waves' part: wave w copies keys 8 w .. + 7 of each step and sums
 // columns 128 w .. + 127 for all rows.
-template <bool BF, bool ONCE>
+template <bool BF, bool ONCE, bool Q8>
 __device__ __forceinline__ void sum_item(const DecodeArgs &a, const DecodeItem &it, const Shared &sh, uint32_t kv_lds, bool careful,
                                          bool &bad_page, f32x16 (&acc)[4][2]) {
     const int lane = threadIdx.x & 63, wave = dev::wave_id() & 3, l31 = lane & 31, lh = lane >> 5;
@@ -323,12 +429,12 @@ __device__ __forceinline__ void sum_item(const DecodeArgs &a, const DecodeItem &
             bad_page = true;
             page = 0;
         }
-        return Copy{a.cache.base + (page * a.cache.page_stride + static_cast<int64_t>(pos & ((1 << shift) - 1)) * kCacheRow) * 2 + cu,
-                    kv_lds + ((t - sh.t0) & (kRing - 1)) * kStepBytes + wave * 1024};
+        return Copy{a.cache.base + page * a.cache.page_bytes + (pos & ((1 << shift) - 1)) * kRowBytes + cu,
+                    kv_lds + ((t - sh.t0) & (kRing - 1)) * kStepBytes<Q8> + wave * 1024};
     };
     auto copy = [&](const Copy &x, int b) {
-        if constexpr (ONCE) dev::copy16_to_lds_once(x.src + b * 128, x.dst + b * kBlockBytes);
-        else dev::copy16_to_lds_free(x.src + b * 128, x.dst + b * kBlockBytes);
+        if constexpr (ONCE) dev::copy16_to_lds_once(x.src + b * 128, x.dst + b * kBlockBytes<Q8>);
+        else dev::copy16_to_lds_free(x.src + b * 128, x.dst + b * kBlockBytes<Q8>);
     };
     auto copy_all = [&](const Copy &x) {
 #pragma unroll
@@ -339,9 +445,10 @@ __device__ __forceinline__ void sum_item(const DecodeArgs &a, const DecodeItem &
     // waves' copies keep the CU's address unit busy for about 900 clocks, nearly
     // as long as both kinds' products take.
     const int kr0 = 8 * lh + ((lane >> 2) & 3);
-    auto step = [&](int t, bool more, Copy &now, int &page) {
+    Source8<BF, ONCE> src(a, it, sh);
+    auto step = [&](int t, bool more, Copy &now, int &page, Stage &from) {
         const int raise = sh.raise[(t - sh.t0) % 3];
-        const uint8_t *vr = sh.ring(t) + 2 * wave * kBlockBytes + 8 * (lane & 1);
+        const uint8_t *vr = sh.ring<Q8>(t) + 2 * wave * kBlockBytes<Q8> + 8 * (lane & 1);
         const uint8_t *pr = sh.weights(t);
         u32x4 pf[2][2], vf[2][4];
         auto read_weights = [&]() {
@@ -355,7 +462,7 @@ __device__ __forceinline__ void sum_item(const DecodeArgs &a, const DecodeItem &
             for (int k = 0; k < 2; ++k)
 #pragma unroll
                 for (int cb = 0; cb < 4; ++cb) {
-                    const uint8_t *blk = vr + (cb >> 1) * kBlockBytes + 16 * k * 128;
+                    const uint8_t *blk = vr + (cb >> 1) * kBlockBytes<Q8> + 16 * k * 128;
                     const int unit = 4 * (cb & 1) + 2 * ((lane >> 4) & 1) + ((lane >> 1) & 1);
                     const u32x2 a0 = dev::read_tr(blk + dev::tile_unit(kr0, unit));
                     const u32x2 a1 = dev::read_tr(blk + dev::tile_unit(kr0 + 4, unit));
@@ -379,11 +486,12 @@ __device__ __forceinline__ void sum_item(const DecodeArgs &a, const DecodeItem &
                 }
         }
         if (careful && (t + 1) * kStepKeys > sh.open) {
-            clean<BF>(sh, t);
+            clean<BF, Q8>(sh, t);
             read_values();
         }
         Copy next = now;
-        if (more) copy(now, 0);
+        uint8_t *place = sh.ring<Q8>(t + 2);
+        if (!Q8 && more) copy(now, 0);
 #pragma unroll
         for (int k = 0; k < 2; ++k)
 #pragma unroll
@@ -392,34 +500,72 @@ __device__ __forceinline__ void sum_item(const DecodeArgs &a, const DecodeItem &
 #pragma unroll
                 for (int rb = 0; rb < 2; ++rb) acc[cb][rb] = dev::mma<BF>(vf[k][cb], pf[k][rb], acc[cb][rb]);
                 __builtin_amdgcn_sched_barrier(0);
-                if (more) copy(now, 1 + 4 * k + cb);
-                if (more && k == 1 && cb == 1) {
-                    next = aim(t + 4, page);
-                    page = page_of(t + 5);
+                if constexpr (Q8) {
+                    if (more && k == 0 && cb == 0) src.store_latent(from, place, 0);
+                    if (more && k == 0 && cb == 2) src.store_latent(from, place, 1);
+                    if (more && k == 1 && cb == 0) {
+                        src.store_rope(from, place);
+                        src.load(from, t + 4);
+                    }
+                } else {
+                    if (more) copy(now, 1 + 4 * k + cb);
+                    if (more && k == 1 && cb == 1) {
+                        next = aim(t + 4, page);
+                        page = page_of(t + 5);
+                    }
                 }
             }
         now = next;
     };
 
-    const int pg0 = page_of(sh.t0), pg1 = page_of(sh.t0 + 1), pg2 = page_of(sh.t0 + 2), pg3 = page_of(sh.t0 + 3);
-    int page = page_of(sh.t0 + 4);
-    copy_all(aim(sh.t0, pg0));
-    copy_all(aim(sh.t0 + 1, pg1));
-    Copy now = aim(sh.t0 + 2, pg2);
-    dev::lds_barrier();                                  // the queries have landed
-    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kBlocks) : "memory");
-    dev::lds_barrier();                                  // step t0 has landed, and the queries have been read
-    copy_all(now);
-    now = aim(sh.t0 + 3, pg3);
-    dev::lds_barrier();                                  // the first maxima
-    for (int t = sh.t0 + 1; t < sh.t1; ++t) {
-        // Step t has landed when only the copies of step t + 1 are in flight.
-        asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kBlocks) : "memory");
+    Stage st[2];
+    Copy now{};
+    int page = 0;
+    if constexpr (Q8) {
+        src.ask(sh.t0);
+        src.load(st[0], sh.t0);
+        src.load(st[1], sh.t0 + 1);
+        dev::lds_barrier();                              // the queries have landed
+        src.store(st[0], sh.ring<Q8>(sh.t0));
+        src.load(st[0], sh.t0 + 2);
+        dev::lds_barrier();                              // step t0 has been written, and the queries have been read
+        src.store(st[1], sh.ring<Q8>(sh.t0 + 1));
+        src.load(st[1], sh.t0 + 3);
+        dev::lds_barrier();                              // the first maxima
+        int t = sh.t0 + 1;
+        for (; t + 1 < sh.t1; t += 2) {
+            dev::lds_barrier();
+            step(t - 1, true, now, page, st[0]);
+            dev::lds_barrier();
+            step(t, true, now, page, st[1]);
+        }
+        if (t < sh.t1) {
+            dev::lds_barrier();
+            step(t - 1, true, now, page, st[0]);
+        }
         dev::lds_barrier();
-        step(t - 1, true, now, page);
+        bad_page = bad_page || src.bad;
+    } else {
+        const int pg0 = page_of(sh.t0), pg1 = page_of(sh.t0 + 1), pg2 = page_of(sh.t0 + 2), pg3 = page_of(sh.t0 + 3);
+        page = page_of(sh.t0 + 4);
+        copy_all(aim(sh.t0, pg0));
+        copy_all(aim(sh.t0 + 1, pg1));
+        now = aim(sh.t0 + 2, pg2);
+        dev::lds_barrier();                              // the queries have landed
+        asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kBlocks) : "memory");
+        dev::lds_barrier();                              // step t0 has landed, and the queries have been read
+        copy_all(now);
+        now = aim(sh.t0 + 3, pg3);
+        dev::lds_barrier();                              // the first maxima
+        for (int t = sh.t0 + 1; t < sh.t1; ++t) {
+            // Step t has landed when only the copies of step t + 1 are in flight.
+            asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kBlocks) : "memory");
+            dev::lds_barrier();
+            step(t - 1, true, now, page, st[0]);
+        }
+        dev::copy_barrier();
     }
-    dev::copy_barrier();
-    step(last, false, now, page);
+    step(last, false, now, page, st[0]);
     float z = 0.0f;
 #pragma unroll
     for (int cb = 0; cb < 4; ++cb)
@@ -436,7 +582,7 @@ __device__ __forceinline__ void sum_item(const DecodeArgs &a, const DecodeItem &
 // then NaN or +inf and the whole row NaN, or it is -inf and the output 0 * inf.)
 // The keys are read from the cache again, eight at a time: this is rare, and a count
 // of them beside the products, in the registers that those leave, spills 673.
-template <bool BF>
+template <bool BF, bool Q8>
 __device__ __forceinline__ void spoil_seen(const DecodeArgs &a, const DecodeItem &it, const Shared &sh, int rows, f32x16 (&acc)[4][2]) {
     const int lane = threadIdx.x & 63, wave = dev::wave_id() & 3, l31 = lane & 31, lh = lane >> 5;
     const int32_t *table = a.cache.table + it.seq * a.cache.table_stride;
@@ -452,8 +598,12 @@ __device__ __forceinline__ void spoil_seen(const DecodeArgs &a, const DecodeItem
             const int pos = min(key + j, it.len - 1), at = pos >> shift;
             int page = dev::ld_uniform(table + min(at, max(cols, 1) - 1));
             if (page < 0 || page >= a.cache.n_pages || at >= cols) page = 0;   // flagged where it was copied
-            const uint8_t *row = a.cache.base + (page * a.cache.page_stride + static_cast<int64_t>(pos & ((1 << shift) - 1)) * kCacheRow) * 2;
-            off[j] = *reinterpret_cast<const uint32_t *>(row + 256 * wave + 4 * lane);
+            const uint8_t *row = a.cache.base + page * a.cache.page_bytes + (pos & ((1 << shift) - 1)) * (Q8 ? kRow8Bytes : kRowBytes);
+            if constexpr (Q8)
+                off[j] = dev::of_fp8<BF, false>(*reinterpret_cast<const uint16_t *>(row + 128 * wave + 2 * lane),
+                                                __uint_as_float(static_cast<uint32_t>(row[kRow8Scales + 4 * wave + (lane >> 4)]) << 23));
+            else
+                off[j] = *reinterpret_cast<const uint32_t *>(row + 256 * wave + 4 * lane);
         }
 #pragma unroll
         for (int j = 0; j < kBatch; ++j) {
@@ -503,7 +653,8 @@ __device__ __forceinline__ DecodeItem take_item(const DecodeArgs &a, int round, 
     const int8v v = dev::ld_uniform(reinterpret_cast<const int8v *>(a.plan.items + static_cast<int64_t>(round) * gridDim.x + blockIdx.x));
     DecodeItem it = __builtin_bit_cast(DecodeItem, v);
     more = it.seq & kItemMore;
-    it.seq &= ~kItemMore;
+    const bool prefix = it.seq & kItemPrefix;
+    it.seq &= ~(kItemMore | kItemPrefix);
     if (__builtin_expect(!planned(a, head), 0)) {
         dev::flag_if(true, a.err, kErrSeq);
         it.n = 0;
@@ -511,13 +662,13 @@ __device__ __forceinline__ DecodeItem take_item(const DecodeArgs &a, int round, 
     }
     sh.t0 = 2 * it.t0;
     sh.t1 = min(2 * it.t1, (it.len + kStepKeys - 1) / kStepKeys);
-    sh.open = it.len - it.n + (a.mask ? 0 : 1);
+    sh.open = prefix ? INT32_MAX : it.len - it.n + (a.mask ? 0 : 1);
     return it;
 }
 
-template <bool BF, bool ONCE>
+template <bool BF, bool ONCE, bool Q8>
 __global__ __launch_bounds__(kThreads, 2) void latent_decode_kernel(DecodeArgs a) {
-    __shared__ __align__(1024) uint8_t s_kv[kRing * kStepBytes];
+    __shared__ __align__(1024) uint8_t s_kv[kRing * kStepBytes<Q8>];
     __shared__ __align__(1024) uint8_t s_p[2 * kTileRows * 64];
     __shared__ float s_red[2 * 2 * kTileRows], s_fac[kTileRows], s_sum[2 * kTileRows];
     __shared__ int s_raise[3], s_bad;
@@ -527,7 +678,7 @@ __global__ __launch_bounds__(kThreads, 2) void latent_decode_kernel(DecodeArgs a
 
     // The two kinds walk the items in loops of their own (and meet at the same
     // barriers): neither then holds registers for the other.
-    bool more = true;
+    bool more = true, bad_page = false;
     Shared sh{s_kv, s_p, s_red, s_fac, s_sum, s_raise, &s_bad, 0, 0, 0};
     if (wave < 4) {
         for (int round = 0; more; ++round) {
@@ -538,7 +689,7 @@ __global__ __launch_bounds__(kThreads, 2) void latent_decode_kernel(DecodeArgs a
             for (int careful = 0; careful < 2; ++careful) {
                 dev::lds_barrier();                      // the buffers of the item (or pass) before are free
                 if (tid == 0) s_bad = s_raise[0] = s_raise[1] = s_raise[2] = 0;
-                score_item<BF>(a, it, sh, rows, careful, m);
+                score_item<BF, ONCE, Q8>(a, it, sh, rows, careful, bad_page, m);
                 dev::lds_barrier();
                 if (!(s_bad && sh.t1 * kStepKeys > sh.open)) break;
             }
@@ -560,7 +711,6 @@ __global__ __launch_bounds__(kThreads, 2) void latent_decode_kernel(DecodeArgs a
         }
     } else {
         const int w = wave - 4;
-        bool bad_page = false;
         for (int round = 0; more; ++round) {
             const DecodeItem it = take_item(a, round, more, sh);
             if (it.n == 0) continue;
@@ -568,8 +718,8 @@ __global__ __launch_bounds__(kThreads, 2) void latent_decode_kernel(DecodeArgs a
             f32x16 acc[4][2];                            // [32 columns][32 rows] blocks of O^T
             for (int careful = 0; careful < 2; ++careful) {
                 dev::lds_barrier();
-                sum_item<BF, ONCE>(a, it, sh, kv_lds, careful, bad_page, acc);
-                if (careful) spoil_seen<BF>(a, it, sh, rows, acc);
+                sum_item<BF, ONCE, Q8>(a, it, sh, kv_lds, careful, bad_page, acc);
+                if (careful) spoil_seen<BF, Q8>(a, it, sh, rows, acc);
                 dev::lds_barrier();
                 if (!(s_bad && sh.t1 * kStepKeys > sh.open)) break;
             }
@@ -597,8 +747,8 @@ __global__ __launch_bounds__(kThreads, 2) void latent_decode_kernel(DecodeArgs a
                                                                        acc[cb][rb][4 * g + 2], acc[cb][rb][4 * g + 3]};
             }
         }
-        dev::flag_if(bad_page, a.err, kErrPage);
     }
+    dev::flag_if(bad_page, a.err, kErrPage);
 }
 
 // Joins the pieces of a row: with M = max m_i, o = sum 2^(m_i - M) O_i / sum
@@ -630,23 +780,38 @@ __global__ __launch_bounds__(256) void join_kernel(DecodeArgs a) {
         float top = -__builtin_inff();
 #pragma unroll 8
         for (int i = 0; i < u.split; ++i) top = fmaxf(top, ml[i * kTileRows * 2]);
+        // Pieces of the group's prefix: the row lies elsewhere in the group's units.
+        const float *pml = nullptr;
+        const f32x4 *ppart = nullptr;
+        if (u.prefix_split) {
+            const int at = u.prefix_row + (live ? r : 0), pr = at % kTileRows;
+            const int64_t slot = u.prefix_slot0 + at / kTileRows * u.prefix_split;
+            pml = a.part_ml + (slot * kTileRows + pr) * 2;
+            ppart = reinterpret_cast<const f32x4 *>(a.part + slot * kTileRows * kLatent) + ((block & ~1) | (pr >> 5)) * 256 + ((lane & 32) | (pr & 31));
+#pragma unroll 8
+            for (int i = 0; i < u.prefix_split; ++i) top = fmaxf(top, pml[i * kTileRows * 2]);
+        }
         const float ms = top == -__builtin_inff() ? 0.0f : top;
         float l = 0.0f;
         f32x16 o;
 #pragma unroll
         for (int i = 0; i < 16; ++i) o[i] = 0.0f;
-        const int p0 = apart ? 0 : u.split * wave / 4, p1 = apart ? u.split : u.split * (wave + 1) / 4;
+        auto add = [&](const float *ml, const f32x4 *part, int split) {
+            const int p0 = apart ? 0 : split * wave / 4, p1 = apart ? split : split * (wave + 1) / 4;
 #pragma unroll 4
-        for (int i = p0; i < p1; ++i) {
-            const float f = __builtin_amdgcn_exp2f(ml[i * kTileRows * 2] - ms);
-            l = __builtin_fmaf(f, ml[i * kTileRows * 2 + 1], l);
+            for (int i = p0; i < p1; ++i) {
+                const float f = __builtin_amdgcn_exp2f(ml[i * kTileRows * 2] - ms);
+                l = __builtin_fmaf(f, ml[i * kTileRows * 2 + 1], l);
 #pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                const f32x4 v = part[static_cast<int64_t>(i) * (kTileRows * kLatent / 4) + 64 * g];
+                for (int g = 0; g < 4; ++g) {
+                    const f32x4 v = part[static_cast<int64_t>(i) * (kTileRows * kLatent / 4) + 64 * g];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) o[4 * g + j] = __builtin_fmaf(f, v[j], o[4 * g + j]);
+                    for (int j = 0; j < 4; ++j) o[4 * g + j] = __builtin_fmaf(f, v[j], o[4 * g + j]);
+                }
             }
-        }
+        };
+        add(ml, part, u.split);
+        if (u.prefix_split) add(pml, ppart, u.prefix_split);
         if (!apart) {
             __syncthreads();
             if (wave) {
@@ -694,13 +859,26 @@ constexpr int kJoinItems = 64;  // pieces whose joining costs as much as a tile
 constexpr int kMinRun = 2;
 constexpr float kTileTime = 1.4f, kPieceTime = 0.06f;   // of 16 pieces' joining
 constexpr int kSortMost = 1024; // sequences that are put in order
+static_assert(kPrefixEntries == kSortMost && kPrefixEntries == kPlanThreads, "an entry to a thread, all of them in LDS");
 constexpr int kItemLanes = 16;  // lanes that write a sequence's items
 
 __device__ __forceinline__ int cut(int tiles, int per) { return max(1, (tiles + per - 1) / per); }
 
+// Groups of sequences that share a prefix (PREFIX).  The prefix is attended by an entry
+// of its own behind the sequences' (at most kSortMost entries in all): the group's
+// tokens, which are neighbours, are its rows, and its keys are the prefix's whole
+// tiles, found through the first sequence's row of the block table.  No more than what
+// every token of the group sees as context is shared, so that nothing of it is
+// masked; the sequences begin behind it.  Both leave pieces for the join.
+struct Groups {
+    const int32_t *start, *prefix;     // [n + 1] first sequences; [n] tokens
+    int n;
+};
+
+template <bool PREFIX>
 __global__ __launch_bounds__(kPlanThreads) void decode_plan_kernel(DecodePlan p, const int32_t *q_start, const int32_t *kv_len,
                                                                    int n_seq, int n_tok, int n_heads, int n_cu, int unit_cap,
-                                                                   int32_t *err) {
+                                                                   Groups groups, int32_t *err) {
     __shared__ int s_tmp[kPlanThreads / 64 + 1];
     __shared__ unsigned long long s_units, s_work;
     __shared__ float s_cost[kPlanThreads / 64];
@@ -719,15 +897,69 @@ __global__ __launch_bounds__(kPlanThreads) void decode_plan_kernel(DecodePlan p,
     bool bad = false;
     unsigned long long my_units = 0, my_work = 0;
     int my_most = 1;
+    // Of a sequence: its group (-1: none).  Of a group: first sequence and behind the
+    // last, the least context of its tokens (later the tiles that it shares), how many
+    // of its sequences have tokens, and the first that does.
+    __shared__ int s_group[PREFIX ? kSortMost : 1], s_from[PREFIX ? kSortMost + 1 : 1], s_least[PREFIX ? kSortMost : 1], s_live[PREFIX ? kSortMost : 1], s_head[PREFIX ? kSortMost : 1];
+    __shared__ int s_groups;
+    const int q_seqs = n_seq;
+    if constexpr (PREFIX) {
+        if (tid == 0) s_groups = groups.n;
+        if (tid <= groups.n) s_from[tid] = groups.start[tid];
+        s_least[tid] = s_head[tid] = INT32_MAX;
+        s_live[tid] = 0;
+        __syncthreads();
+        if (tid < groups.n && (s_from[tid] < 0 || s_from[tid + 1] < s_from[tid] || s_from[tid + 1] > n_seq)) {
+            bad = true;
+            s_groups = 0;                                // nothing is shared
+        }
+        __syncthreads();
+        int g = -1;
+        if (tid < n_seq && s_groups) {
+            int lo = 0, hi = s_groups;                   // the last group that begins at or before the sequence
+            while (lo < hi) {
+                const int mid = (lo + hi) / 2;
+                if (s_from[mid] <= tid) lo = mid + 1;
+                else hi = mid;
+            }
+            if (lo > 0 && tid < s_from[lo]) g = lo - 1;
+        }
+        s_group[tid] = g;
+        if (g >= 0) {
+            const int q0 = q_start[tid], q1 = q_start[tid + 1], len = kv_len[tid];
+            const bool ok = q0 >= 0 && q1 >= q0 && q1 <= n_tok && len >= 0 && len <= INT32_MAX - 2 * kTileKeys;
+            if (!ok || q1 > q0) atomicMin(&s_least[g], ok ? len - (q1 - q0) : 0);
+            if (ok && q1 > q0) {
+                atomicAdd(&s_live[g], 1);
+                atomicMin(&s_head[g], tid);
+            }
+        }
+        __syncthreads();
+        if (tid < groups.n) {
+            const int g0 = s_from[tid];
+            int tiles = 0, tokens = 0, q0 = 0;
+            if (tid < s_groups && s_live[tid] > 1) {     // every sequence of the group is in order
+                tiles = max(0, min(groups.prefix[tid], s_least[tid])) / kTileKeys;
+                q0 = q_start[g0];
+                tokens = tiles ? q_start[s_from[tid + 1]] - q0 : 0;
+            }
+            s_least[tid] = tiles;
+            s_seq[n_seq + tid] = int4{static_cast<int>((static_cast<int64_t>(tokens) * n_heads + kTileRows - 1) / kTileRows), tiles, 0, 0};
+            s_at[n_seq + tid] = int4{q0, tokens, tiles * kTileKeys, s_head[tid]};
+        }
+        __syncthreads();
+    }
     for (int b = tid; b < n_seq; b += kPlanThreads) {
         const int q0 = q_start[b], q1 = q_start[b + 1], len = kv_len[b];
         const bool ok = q0 >= 0 && q1 >= q0 && q1 <= n_tok && len >= 0 && len <= INT32_MAX - 2 * kTileKeys;
         bad = bad || !ok;
         const int units = ok ? static_cast<int>((static_cast<int64_t>(q1 - q0) * n_heads + kTileRows - 1) / kTileRows) : 0;
-        const int tiles = ok ? (len + kTileKeys - 1) / kTileKeys : 0;
+        int tiles = ok ? (len + kTileKeys - 1) / kTileKeys : 0, behind = 0;
+        if (PREFIX && s_group[b] >= 0 && units) behind = s_least[s_group[b]];
+        tiles -= behind;
         if (b < kSortMost) {
             s_seq[b] = int4{units, tiles, 0, 0};
-            s_at[b] = int4{q0, q1 - q0, len, 0};
+            s_at[b] = int4{q0, q1 - q0, len, behind};
         } else {
             seq[b] = int4{units, tiles, 0, 0};
         }
@@ -735,24 +967,61 @@ __global__ __launch_bounds__(kPlanThreads) void decode_plan_kernel(DecodePlan p,
         my_work += static_cast<unsigned long long>(units) * tiles;
         if (units) my_most = max(my_most, tiles);
     }
+    auto total = [&]() {
 #pragma unroll
-    for (int o = 32; o; o >>= 1) {
-        my_units += __shfl_xor(my_units, o, 64);
-        my_work += __shfl_xor(my_work, o, 64);
-        my_most = max(my_most, __shfl_xor(my_most, o, 64));
+        for (int o = 32; o; o >>= 1) {
+            my_units += __shfl_xor(my_units, o, 64);
+            my_work += __shfl_xor(my_work, o, 64);
+            my_most = max(my_most, __shfl_xor(my_most, o, 64));
+        }
+        if (lane == 0) {
+            atomicAdd(&s_units, my_units);
+            atomicAdd(&s_work, my_work);
+            atomicMax(&s_most, my_most);
+        }
+        __syncthreads();
+    };
+    if constexpr (PREFIX) {
+        n_seq += groups.n;
+        if (tid < groups.n) {
+            const int4 s = s_seq[q_seqs + tid];
+            my_units += s.x;
+            my_work += static_cast<unsigned long long>(s.x) * s.y;
+            if (s.x) my_most = max(my_most, s.y);
+        }
     }
-    if (lane == 0) {
-        atomicAdd(&s_units, my_units);
-        atomicAdd(&s_work, my_work);
-        atomicMax(&s_most, my_most);
+    total();
+    if constexpr (PREFIX) {
+        // A piece of every unit has to find room: else each sequence attends to all of its keys.
+        if (s_units > static_cast<unsigned long long>(min(p.slot_cap, 4 * n_cu))) {
+            n_seq = q_seqs;
+            my_units = my_work = 0;
+            my_most = 1;
+            if (tid < n_seq) {
+                s_seq[tid].y += s_at[tid].w;
+                s_at[tid].w = 0;
+                const int4 s = s_seq[tid];
+                my_units = s.x;
+                my_work = static_cast<unsigned long long>(s.x) * s.y;
+                if (s.x) my_most = max(my_most, s.y);
+            }
+            __syncthreads();
+            if (tid == 0) {
+                s_units = s_work = 0;
+                s_most = 1;
+            }
+            __syncthreads();
+            total();
+        }
     }
-    __syncthreads();
     const unsigned long long units = s_units;
     const int most = s_most;
-    if (units > static_cast<unsigned long long>(unit_cap)) {   // sequences that overlap: nothing is planned
+    if (n_seq == q_seqs && units > static_cast<unsigned long long>(unit_cap)) {   // sequences that overlap: nothing is planned
         bad = true;
         n_seq = 0;
     }
+    // Whether an entry's pieces are joined with others even if it is not cut.
+    auto shares = [&](int b) { return PREFIX && (b >= q_seqs || s_at[b].w > 0); };
     // Items at a run length, one wave per candidate; 2^24 stands for any more.
     auto items_at = [&](int per) {
         unsigned long long n = 0;
@@ -842,23 +1111,42 @@ __global__ __launch_bounds__(kPlanThreads) void decode_plan_kernel(DecodePlan p,
         const int b = b0 + tid >= n_seq ? n_seq : sorted ? s_order[b0 + tid] : b0 + tid;
         int4 s = b >= n_seq ? int4{0, 0, 0, 0} : b < kSortMost ? s_seq[b] : seq[b];
         const int split = cut(s.y, best), count = s.x * split;
+        const bool parts = b < n_seq && (split > 1 || shares(b));
+        const int units_joined = parts && (!PREFIX || b < q_seqs) ? s.x : 0;
         int total;
         const int at = n_items + dev::block_exclusive_scan<kPlanThreads>(count, s_tmp, &total);
         n_items += total;
-        const int slot = n_slots + dev::block_exclusive_scan<kPlanThreads>(split > 1 ? count : 0, s_tmp, &total);
+        const int slot = n_slots + dev::block_exclusive_scan<kPlanThreads>(parts ? count : 0, s_tmp, &total);
         n_slots += total;
-        const int join = n_joins + dev::block_exclusive_scan<kPlanThreads>(split > 1 ? s.x : 0, s_tmp, &total);
+        const int join = n_joins + dev::block_exclusive_scan<kPlanThreads>(units_joined, s_tmp, &total);
         n_joins += total;
         if (b < n_seq) {
             s.z = at;
-            s.w = split > 1 ? slot : -1;
+            s.w = parts ? slot : -1;
             if (b < kSortMost) s_seq[b] = s;
             else seq[b] = s;
-            if (split > 1 && s.x) atomicMax(&s_most, split);
-            if (split > 1 && slot + count <= p.slot_cap && join + s.x <= p.join_cap) {
+        }
+        if constexpr (PREFIX) __syncthreads();           // the groups' slots
+        if (units_joined) {
+            JoinUnit u{};
+            if constexpr (PREFIX)
+                if (shares(b)) {
+                    const int g = q_seqs + s_group[b];
+                    u.prefix_row = (s_at[b].x - s_at[g].x) * n_heads;
+                    u.prefix_slot0 = s_seq[g].w;
+                    u.prefix_split = cut(s_seq[g].y, best);
+                }
+            atomicMax(&s_most, split + u.prefix_split);
+            if (slot + count <= p.slot_cap && join + s.x <= p.join_cap) {
                 const int q0 = b < kSortMost ? s_at[b].x : q_start[b], rows = (b < kSortMost ? s_at[b].y : q_start[b + 1] - q0) * n_heads;
-                for (int i = 0; i < s.x; ++i)
-                    p.joins[join + i] = JoinUnit{q0 * n_heads + i * kTileRows, min(kTileRows, rows - i * kTileRows), slot + i * split, split};
+                u.split = split;
+                for (int i = 0; i < s.x; ++i) {
+                    u.out_row = q0 * n_heads + i * kTileRows;
+                    u.rows = min(kTileRows, rows - i * kTileRows);
+                    u.slot0 = slot + i * split;
+                    p.joins[join + i] = u;
+                    u.prefix_row += kTileRows;
+                }
             }
         }
     }
@@ -892,6 +1180,8 @@ __global__ __launch_bounds__(kPlanThreads) void decode_plan_kernel(DecodePlan p,
                 s = seq[b];
                 at = int4{q_start[b], q_start[b + 1] - q_start[b], kv_len[b], 0};
             }
+            const bool prefix = PREFIX && b >= q_seqs;
+            const int behind = PREFIX && !prefix ? at.w : 0, seq_bits = prefix ? at.w | kItemPrefix : b;
             const int split = cut(s.y, best), each = s.y / split, over = s.y - each * split;
             // Neighbouring items: the units of one run of keys.
             for (int i = tid % kItemLanes; i < s.x * split; i += kItemLanes) {
@@ -900,9 +1190,9 @@ __global__ __launch_bounds__(kPlanThreads) void decode_plan_kernel(DecodePlan p,
                 it.q0 = at.x;
                 it.n = at.y;
                 it.len = at.z;
-                it.seq = b | ((s.z + i) / n_cu + 1 < rounds ? kItemMore : 0);
+                it.seq = seq_bits | ((s.z + i) / n_cu + 1 < rounds ? kItemMore : 0);
                 it.row0 = u * kTileRows;
-                it.t0 = c * each + min(c, over);
+                it.t0 = behind + c * each + min(c, over);
                 it.t1 = it.t0 + each + (c < over);
                 it.slot = s.w < 0 ? -1 : s.w + u * split + c;
                 p.items[place(s.z + i)] = it;
@@ -920,22 +1210,31 @@ __global__ __launch_bounds__(kPlanThreads) void decode_plan_kernel(DecodePlan p,
 }  // namespace
 
 hipError_t launch_decode_plan(const DecodePlan &p, const int32_t *q_start, const int32_t *kv_len, int n_seq, int n_tok,
-                              int n_heads, int n_cu, int32_t *err, hipStream_t s) {
+                              int n_heads, int n_cu, const int32_t *group_start, const int32_t *prefix_len, int n_groups, int32_t *err,
+                              hipStream_t s) {
     const int unit_cap = static_cast<int>(std::min<int64_t>(INT32_MAX, static_cast<int64_t>(n_tok) * n_heads / kTileRows + n_seq));
-    launch(decode_plan_kernel, 1u, kPlanThreads, 0, s, p, q_start, kv_len, n_seq, n_tok, n_heads, n_cu, unit_cap, err);
+    const Groups groups{group_start, prefix_len, n_groups};
+    launch(n_groups ? decode_plan_kernel<true> : decode_plan_kernel<false>, 1u, kPlanThreads, 0, s, p, q_start, kv_len, n_seq, n_tok, n_heads, n_cu, unit_cap,
+           groups, err);
     return hipGetLastError();
 }
 
-hipError_t launch_latent_decode(const DecodeArgs &a, bool bf16, int n_cu, hipStream_t s) {
+template <bool Q8>
+static void launch_decode_kernel(const DecodeArgs &a, bool bf16, bool once, int n_cu, hipStream_t s) {
+    launch(once ? (bf16 ? latent_decode_kernel<true, true, Q8> : latent_decode_kernel<false, true, Q8>)
+                : (bf16 ? latent_decode_kernel<true, false, Q8> : latent_decode_kernel<false, false, Q8>),
+           static_cast<unsigned>(n_cu), kThreads, 0, s, a);
+}
+
+hipError_t launch_latent_decode(const DecodeArgs &a, bool bf16, bool cache8, bool prefixes, int n_cu, hipStream_t s) {
     // Where a sequence's rows fill one item (on the average: the sequences' own
     // counts are the device's), its keys are read once and not kept in the
     // caches: 64 sequences up to 12k tokens 88 -> 81 us.  Items that share keys
     // lose by it (trees of 25 nodes 173 -> 178 us), and by a test at each
     // copy instead of two kernels (191 us).
-    const bool once = static_cast<int64_t>(a.n_tok) * a.n_heads <= static_cast<int64_t>(a.n_seq) * kTileRows;
-    launch(once ? (bf16 ? latent_decode_kernel<true, true> : latent_decode_kernel<false, true>)
-                : (bf16 ? latent_decode_kernel<true, false> : latent_decode_kernel<false, false>),
-           static_cast<unsigned>(n_cu), kThreads, 0, s, a);
+    const bool once = !prefixes && static_cast<int64_t>(a.n_tok) * a.n_heads <= static_cast<int64_t>(a.n_seq) * kTileRows;
+    if (cache8) launch_decode_kernel<true>(a, bf16, once, n_cu, s);
+    else launch_decode_kernel<false>(a, bf16, once, n_cu, s);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     const unsigned blocks = static_cast<unsigned>(std::min<int64_t>(static_cast<int64_t>(a.join_most) * kOutBlocks, 8 * n_cu));

@@ -10,6 +10,14 @@ namespace coli {
 constexpr int kLatent = 512;             // latent values of one cached token: keys and values of every head
 constexpr int kRope = 64;                // its rotary key values
 constexpr int kCacheRow = kLatent + kRope;
+constexpr int kRowBytes = 2 * kCacheRow;
+// A row of an 8-bit cache: the latent values in e4m3, the rotary ones in 16 bits, a
+// scale's exponent (biased by 127) for each 32 latent values.
+constexpr int kScaleGroup = 32;
+constexpr int kRow8Rope = kLatent, kRow8Scales = kLatent + 2 * kRope;
+constexpr int kRow8Bytes = kRow8Scales + kLatent / kScaleGroup;
+constexpr int kPrefixEntries = 1024;     // sequences and groups of a plan whose groups share prefixes
+constexpr int kBeamMost = 64;            // beams of a group, and continuations kept of one
 constexpr int kTileKeys = 64;            // cached tokens per attention tile
 constexpr int kTileRows = 64;            // (token, head) rows per absorbed-attention item
 constexpr int kVerifyMaxNodes = 1024;    // drafted nodes of one sequence
@@ -25,14 +33,17 @@ constexpr int32_t kErrNoMass = 8;     // no token of a row has a positive probab
 // of its rows afterwards.  Items are laid out in rounds of one per workgroup;
 // n == 0 is a place without one.
 struct alignas(32) DecodeItem {
-    int32_t q0, n, len, seq;   // first token, tokens and cached length of the sequence; seq | kItemMore: rounds follow
+    int32_t q0, n, len, seq;   // first token, tokens and cached length of the sequence; seq | kItemMore: rounds follow;
+                               // | kItemPrefix: a group's tokens and prefix, seq its first sequence
     int32_t row0, t0, t1, slot;
 };
-constexpr int32_t kItemMore = 1 << 30;
+constexpr int32_t kItemMore = 1 << 30, kItemPrefix = 1 << 29;
 // Rows whose pieces are joined: `rows` output rows from out_row, the partials
-// slot0 .. slot0 + split - 1.
-struct alignas(16) JoinUnit {
+// slot0 .. slot0 + split - 1, and of the group's prefix: the unit's first row is row
+// prefix_row of the group, whose unit i has slots prefix_slot0 + i prefix_split ...
+struct alignas(32) JoinUnit {
     int32_t out_row, rows, slot0, split;
+    int32_t prefix_row, prefix_slot0, prefix_split, unused;
 };
 struct DecodePlan {
     int32_t *head;             // [4] join units, the most pieces of one, tokens, sequences
@@ -44,7 +55,7 @@ struct DecodePlan {
 
 struct CacheView {
     uint8_t *base;
-    int64_t page_stride;       // elements from one page to the next
+    int64_t page_bytes;        // from one page to the next
     int n_pages, page_shift;
     const int32_t *table;      // [n_seq x table_cols] page numbers
     int64_t table_stride;
@@ -92,7 +103,7 @@ struct AppendArgs {
     const int64_t *slots;
     int n_tok, n_heads;
     uint8_t *cache;
-    int64_t page_stride;
+    int64_t page_bytes;
     int n_pages, page_shift;
     const uint8_t *q_pe;       // or NULL
     int64_t q_tok, q_head;
@@ -103,10 +114,44 @@ struct AppendArgs {
 struct KeepArgs {
     CacheView cache;
     int n_layers;
-    int64_t layer_stride;
+    int64_t layer_bytes;
     const int32_t *q_start, *kv_len, *path;
     int64_t path_stride;
     int path_cols, n_seq, n_tok;
+    int32_t *err;
+};
+
+struct ReadArgs {
+    CacheView cache;
+    const int32_t *first, *k_start;   // first may be NULL
+    int n_seq, n_rows;
+    uint8_t *out;              // [n_rows x 576]
+    int64_t out_stride;        // elements
+    int32_t *err;
+};
+
+struct ReorderArgs {
+    CacheView cache;
+    int n_layers;
+    int64_t layer_bytes;
+    const int32_t *kv_len, *parents;   // [n_groups x beams]
+    int n_groups, beams;
+    int32_t *out_table;
+    int64_t out_stride;
+    int32_t *err;
+};
+
+struct SelectArgs {
+    const uint8_t *logits;     // [n_groups x beams x vocab] rows
+    int64_t stride;            // elements
+    int kind;                  // coli_prob
+    int vocab, n_groups, beams, keep;
+    const float *scores;       // [n_groups x beams]
+    float *out_scores;         // [n_groups x keep]
+    int32_t *parents, *tokens;
+    uint64_t *best;            // scratch: [rows of a launch x chunks x keep]
+    float2 *sums;              // [rows of a launch x chunks] maximum and sum
+    int64_t best_cap, sums_cap;
     int32_t *err;
 };
 
@@ -126,11 +171,15 @@ struct VerifyArgs {
     int32_t *err;
 };
 
-hipError_t launch_append(const AppendArgs &a, bool bf16, hipStream_t s);
-hipError_t launch_keep(const KeepArgs &a, hipStream_t s);
+hipError_t launch_append(const AppendArgs &a, bool bf16, bool cache8, hipStream_t s);
+hipError_t launch_keep(const KeepArgs &a, bool cache8, hipStream_t s);
+hipError_t launch_read(const ReadArgs &a, bool bf16, bool cache8, hipStream_t s);
+hipError_t launch_reorder(const ReorderArgs &a, bool cache8, hipStream_t s);
+hipError_t launch_select(const SelectArgs &a, int n_cu, hipStream_t s);
 hipError_t launch_decode_plan(const DecodePlan &p, const int32_t *q_start, const int32_t *kv_len, int n_seq, int n_tok,
-                              int n_heads, int n_cu, int32_t *err, hipStream_t s);
-hipError_t launch_latent_decode(const DecodeArgs &a, bool bf16, int n_cu, hipStream_t s);
+                              int n_heads, int n_cu, const int32_t *group_start, const int32_t *prefix_len, int n_groups, int32_t *err,
+                              hipStream_t s);
+hipError_t launch_latent_decode(const DecodeArgs &a, bool bf16, bool cache8, bool prefixes, int n_cu, hipStream_t s);
 hipError_t launch_latent_prompt(PromptArgs a, bool bf16, int nope, int n_cu, hipStream_t s);
 hipError_t launch_verify(const VerifyArgs &a, int n_cu, hipStream_t s);
 

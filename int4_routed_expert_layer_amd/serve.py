@@ -1,11 +1,15 @@
 """Thin ctypes layer over the serving operators of include/coli_moe.h: the
-paged latent cache, latent attention (absorbed and expanded) and the
-verification of drafted tokens.
+paged latent cache (in 16 or 8 bits), latent attention (absorbed and expanded),
+the verification of drafted tokens and beam search.
 
 The pages' engine keeps 576 values a token in place of 32,768 (README "Come
 funziona", compressed attention state) and drafts tokens that the main model
 verifies in one batched forward; the operators are that step's attention and
 acceptance, next to the expert layer of ``binding``.
+
+A cache of the handle's 16-bit type has rows of 576 values, one of torch.uint8
+rows of 656 bytes (``ROW8``: 512 e4m3 values, 64 16-bit rotary ones, 16 scale
+exponents); every call that takes a cache takes either.
 
 Tensors are checked here (device, type, shape, innermost stride), because the
 C ABI sees addresses; sizes and alignment are checked there.  Work goes to
@@ -21,11 +25,16 @@ from . import binding as B
 
 LATENT, ROPE = 512, 64
 ROW = LATENT + ROPE
+GROUP = 32                                    # latent values of an 8-bit row that share a scale
+ROW8 = LATENT + 2 * ROPE + LATENT // GROUP    # bytes of an 8-bit row
 HALF = {"bf16": (0, torch.bfloat16), "f16": (1, torch.float16)}
 PROBS = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 
 _append, _plan, _decode = B.lib.coli_latent_append, B.lib.coli_latent_plan, B.lib.coli_latent_decode
 _prompt, _verify, _keep = B.lib.coli_latent_prompt, B.lib.coli_draft_verify, B.lib.coli_latent_keep
+_append8, _decode8, _keep8 = B.lib.coli_latent8_append, B.lib.coli_latent8_decode, B.lib.coli_latent8_keep
+_read, _plan_shared = B.lib.coli_latent_read, B.lib.coli_latent_plan_shared
+_select, _reorder = B.lib.coli_beam_select, B.lib.coli_beam_reorder
 
 
 def _raw_stream(index):
@@ -126,13 +135,22 @@ class Serve:
         return t.shape
 
     def _cache(self, cache, layers=()):
-        """Address, page stride and pages; `layers` is () or the leading (n_layers,)."""
+        """Address, page stride, pages and whether it is of 8 bits; `layers` is () or the leading (n_layers,)."""
         pages = self._sizes("cache", cache, 3 + len(layers))[-3]
-        at = self._rows("cache", cache, self.dtype, (*layers, pages, self.page_size, ROW))
+        eight = cache.dtype is torch.uint8
+        width = ROW8 if eight else ROW
+        at = self._rows("cache", cache, torch.uint8 if eight else self.dtype, (*layers, pages, self.page_size, width))
         page, row = cache.stride()[-3:-1]
-        if row != ROW and self.page_size > 1:
+        if row != width and self.page_size > 1:
             raise ValueError("the rows of a cache page must be contiguous")
-        return at, page if pages > 1 else max(page, self.page_size * ROW), pages
+        return at, page if pages > 1 else max(page, self.page_size * width), pages, eight
+
+    def _layers(self, cache):
+        """The same of a cache with or without a leading dimension of layers, and their number and stride."""
+        if isinstance(cache, torch.Tensor) and cache.dim() == 4:
+            n = cache.shape[0]
+            return *self._cache(cache, (n,)), n, cache.stride()[0]
+        return *self._cache(cache), 1, 0
 
     def _table(self, block_table, n_seq):
         cols = self._sizes("block_table", block_table, 2)[1]
@@ -157,7 +175,7 @@ class Serve:
 
         c [T, 576], norm_weight [512], cos and sin fp32 [n_positions, 32],
         positions int32 [T], slots int64 [T] (negative: not cached), cache
-        [n_pages, page_size, 576].  Returns the turned q_pe [T, n_heads, 64], or
+        [n_pages, page_size, 576], or 656 bytes a row.  Returns the turned q_pe [T, n_heads, 64], or
         None without q_pe."""
         n = self._sizes("c", c, 2)[0]
         n_pos = self._sizes("cos", cos, 2)[0]
@@ -167,7 +185,7 @@ class Serve:
         psin = self._dense("sin", sin, torch.float32, (n_pos, ROPE // 2))
         ppos = self._dense("positions", positions, torch.int32, (n,))
         pslot = self._dense("slots", slots, torch.int64, (n,))
-        base, page, pages = self._cache(cache)
+        base, page, pages, eight = self._cache(cache)
         pq = po = None
         qt = qh = 0
         if q_pe is not None:
@@ -177,25 +195,38 @@ class Serve:
             q_out, po = self._out("q_out", q_out, shape, self.dtype)
         elif q_out is not None:
             raise ValueError("q_out without q_pe")
-        self._call(_append, pc, c.stride()[0], pw, eps, pcos, psin, n_pos, 1 if interleaved else 0, ppos, pslot, n, base, page, pages, pq, qt, qh, po)
+        self._call(_append8 if eight else _append, pc, c.stride()[0], pw, eps, pcos, psin, n_pos, 1 if interleaved else 0, ppos, pslot, n, base, page, pages, pq, qt, qh, po)
         return q_out
 
-    def plan(self, q_start, kv_len, n_tok=None):
+    def plan(self, q_start, kv_len, n_tok=None, group_start=None, prefix_len=None):
         """Plan the absorbed attention of a step (coli_latent_plan): q_start
         int32 [B + 1], kv_len int32 [B].  n_tok is the number of tokens of the
-        step; if not given it is read from q_start, a synchronising copy."""
+        step; if not given it is read from q_start, a synchronising copy.
+
+        With group_start int32 [G + 1] and prefix_len int32 [G] the sequences
+        group_start[g] .. group_start[g + 1] - 1 begin with the same prefix_len[g]
+        cached tokens, which are attended to once for all of them
+        (coli_latent_plan_shared)."""
         ps, n_seq = self._starts("q_start", q_start)
         pl = self._dense("kv_len", kv_len, torch.int32, (n_seq,))
+        if (group_start is None) != (prefix_len is None):
+            raise ValueError("group_start and prefix_len go together")
+        if group_start is not None:
+            pg, groups = self._starts("group_start", group_start)
+            pp = self._dense("prefix_len", prefix_len, torch.int32, (groups,))
         if n_tok is None:
             n_tok = int(q_start[-1])
-        self._call(_plan, ps, pl, n_seq, n_tok)
+        if group_start is None:
+            self._call(_plan, ps, pl, n_seq, n_tok)
+        else:
+            self._call(_plan_shared, ps, pl, n_seq, n_tok, pg, pp, groups)
         self._planned = (n_seq, n_tok)
 
     def decode(self, q_lat, q_pe, cache, block_table, scale, tree_mask=None, return_lse=False, out=None, lse=None):
         """Absorbed attention of the planned step (coli_latent_decode).
 
         q_lat [T, n_heads, 512], q_pe [T, n_heads, 64], cache [n_pages,
-        page_size, 576], block_table int32 [B, max_pages], tree_mask int64
+        page_size, 576] or [..., 656] bytes, block_table int32 [B, max_pages], tree_mask int64
         [T, words] of ancestor bits or None for chains.  Returns out [T,
         n_heads, 512], or (out, lse fp32 [T, n_heads])."""
         if self._planned is None:
@@ -204,7 +235,7 @@ class Serve:
         h = self.dims.n_heads
         pl = self._rows("q_lat", q_lat, self.dtype, (n, h, LATENT))
         pp = self._rows("q_pe", q_pe, self.dtype, (n, h, ROPE))
-        base, page, pages = self._cache(cache)
+        base, page, pages, eight = self._cache(cache)
         table, row, cols = self._table(block_table, n_seq)
         words, pm = 0, None
         if tree_mask is not None:
@@ -216,7 +247,7 @@ class Serve:
             lse, pe = self._out("lse", lse, (n, h), torch.float32)
         lt, lh, _ = q_lat.stride()
         qt, qh, _ = q_pe.stride()
-        self._call(_decode, pl, lt, lh, pp, qt, qh, base, page, pages, table, row, cols, pm, words, scale, n, po, pe)
+        self._call(_decode8 if eight else _decode, pl, lt, lh, pp, qt, qh, base, page, pages, table, row, cols, pm, words, scale, n, po, pe)
         return out if pe is None else (out, lse)
 
     def prompt(self, q, kv, k_pe, q_start, k_start, scale, causal=True, return_lse=False, out=None, lse=None):
@@ -280,22 +311,85 @@ class Serve:
 
     def keep(self, cache, block_table, q_start, kv_len, path, n_tok=None):
         """Move the accepted nodes' cache rows together (coli_latent_keep), in
-        place: cache [n_pages, page_size, 576], or [n_layers, ...] for every
-        layer in one launch; path int32 [B, cols] as ``verify`` returns it."""
-        layers, layer_stride, lead = 1, 0, ()
-        if isinstance(cache, torch.Tensor) and cache.dim() == 4:
-            layers, layer_stride = cache.shape[0], cache.stride()[0]
-            lead = (layers,)
-            if layers == 0:
-                return
-        base, page, pages = self._cache(cache, lead)
+        place: cache [n_pages, page_size, 576] (or 656 bytes a row), or [n_layers, ...]
+        for every layer in one launch; path int32 [B, cols] as ``verify`` returns it."""
+        if isinstance(cache, torch.Tensor) and cache.dim() == 4 and cache.shape[0] == 0:
+            return
+        base, page, pages, eight, layers, layer_stride = self._layers(cache)
         ps, n_seq = self._starts("q_start", q_start)
         pl = self._dense("kv_len", kv_len, torch.int32, (n_seq,))
         table, row, cols = self._table(block_table, n_seq)
         most = self._sizes("path", path, 2)[1]
         pp = self._rows("path", path, torch.int32, (n_seq, most))
-        self._call(_keep, base, page, pages, layers, layer_stride, table, row, cols, ps, pl, n_seq, self.dims.max_tokens if n_tok is None else n_tok,
+        self._call(_keep8 if eight else _keep, base, page, pages, layers, layer_stride, table, row, cols, ps, pl, n_seq, self.dims.max_tokens if n_tok is None else n_tok,
                    pp, path.stride()[0], most)
+
+    def read(self, cache, block_table, k_start, n_rows=None, first=None, out=None):
+        """Cached rows as 16-bit values, one sequence behind the other (coli_latent_read).
+
+        Row k_start[b] + i of the result [n_rows, 576] is position first[b] + i of
+        sequence b (first None: from position 0); k_start int32 [B + 1], first int32
+        [B].  n_rows, if neither it nor out is given, is read from k_start, a
+        synchronising copy.  Rows of out that no sequence covers stay as they are
+        (those of a new tensor are unspecified)."""
+        base, page, pages, eight = self._cache(cache)
+        ps, n_seq = self._starts("k_start", k_start)
+        table, row, cols = self._table(block_table, n_seq)
+        pf = None if first is None else self._dense("first", first, torch.int32, (n_seq,))
+        if n_rows is None:
+            n_rows = int(k_start[-1]) if out is None else self._sizes("out", out, 2)[0]
+        if n_rows < 0:
+            raise ValueError(f"n_rows {n_rows} must be >= 0")
+        if out is None:
+            out = torch.empty(n_rows, ROW, dtype=self.dtype, device=self.device)
+        po = self._rows("out", out, self.dtype, (n_rows, ROW))
+        self._call(_read, 1 if eight else 0, base, page, pages, table, row, cols, pf, ps, n_seq, n_rows, po, out.stride()[0] if n_rows > 1 else ROW)
+        return out
+
+    def beam_select(self, logits, scores, keep):
+        """The best continuations of each group's beams (coli_beam_select).
+
+        logits [n_groups * beams, vocab] (fp32, bf16 or f16), scores fp32 [n_groups,
+        beams].  Returns scores fp32, parents (the beam within the group) and tokens,
+        int32, [n_groups, keep] each, from the best down; -inf, -1, -1 where there
+        are fewer."""
+        n, vocab = self._sizes("logits", logits, 2)
+        groups, beams = self._sizes("scores", scores, 2)
+        kind = PROBS.get(logits.dtype)
+        if kind is None:
+            raise TypeError(f"logits is {logits.dtype}, must be one of {sorted(map(str, PROBS))}")
+        if n != groups * beams:
+            raise ValueError(f"logits has {n} rows, must have one for each of the {groups * beams} scores")
+        pl = self._rows("logits", logits, logits.dtype, (n, vocab))
+        ps = self._dense("scores", scores, torch.float32, (groups, beams))
+        if keep < 1:
+            raise ValueError(f"keep {keep} must be >= 1")
+        best = torch.empty(groups, keep, dtype=torch.float32, device=self.device)
+        both = torch.empty(2, groups, keep, dtype=torch.int32, device=self.device)
+        parents, tokens = both[0], both[1]
+        self._call(_select, pl, logits.stride()[0] if n > 1 else vocab, kind, vocab, ps, groups, beams, keep, best.data_ptr(), parents.data_ptr(), tokens.data_ptr())
+        return best, parents, tokens
+
+    def beam_reorder(self, cache, block_table, kv_len, parents, out=None):
+        """The cache and block tables of the beams that go on (coli_beam_reorder).
+
+        parents int32 [n_groups, beams]: the beam of its group that each place
+        continues, -1 for none; kv_len int32 [n_groups * beams], equal within a
+        group; block_table [n_groups * beams, cols].  Rows of shared last pages are
+        copied within cache ([n_pages, page_size, ...] or [n_layers, ...], all layers
+        in one launch).  Returns the new block table."""
+        groups, beams = self._sizes("parents", parents, 2)
+        pp = self._dense("parents", parents, torch.int32, (groups, beams))
+        n = groups * beams
+        table, row, cols = self._table(block_table, n)
+        pl = self._dense("kv_len", kv_len, torch.int32, (n,))
+        base, page, pages, eight, layers, layer_stride = self._layers(cache)
+        if out is None:
+            out = torch.empty(n, cols, dtype=torch.int32, device=self.device)
+        po = self._rows("out", out, torch.int32, (n, cols))
+        self._call(_reorder, 1 if eight else 0, base, page, pages, layers, layer_stride, table, row if n > 1 else cols, cols, pl, pp, groups, beams, po,
+                   out.stride()[0] if n > 1 else cols)
+        return out
 
     def device_errors(self) -> int:
         """Read and clear the device error flags (synchronises the device)."""
