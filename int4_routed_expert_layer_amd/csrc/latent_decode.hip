@@ -49,14 +49,17 @@ using dev::u32x4;
 constexpr int kStepKeys = 32;
 constexpr int kBlocks = kCacheRow / 64;                  // 64-column blocks of a cached row: 8 latent, 1 rotary
 constexpr int kLatentBlocks = kLatent / 64;
-// Distance of a step's blocks in LDS.  Values of an 8-bit cache are written there by
-// the waves, 32 lanes to a key: 16 bytes between the blocks put a write's units, which
-// lie in eight of them, on different banks.
+constexpr int kBlockBytes = kStepKeys * 128;
+constexpr int kStepBytes = kBlocks * kBlockBytes;        // 36 KB
+// Steps in LDS.  Of a 16-bit cache: one that is summed, one that is scored and two on
+// their way.  Those of an 8-bit cache on their way lie apart, as they come; a third place
+// is being written.
 template <bool Q8>
-constexpr int kBlockBytes = kStepKeys * 128 + (Q8 ? 16 : 0);
+constexpr int kRing = Q8 ? 3 : 4;
+constexpr int kRawBytes = kStepKeys / 4 * kRow8Bytes;    // a summing wave's share of a step on its way
+constexpr int kWeightBytes = 2 * kTileRows * 64;
 template <bool Q8>
-constexpr int kStepBytes = kBlocks * kBlockBytes<Q8>;    // 36 KB
-constexpr int kRing = 4;
+constexpr int kKeyBytes = kRing<Q8> * kStepBytes;
 constexpr int kDepth = kCacheRow / 32;                   // K steps of the first product
 // The running maximum of a row moves only when a step exceeds it by more than
 // 2^kSlack: the accumulator is then rarely rescaled, and probabilities stay
@@ -96,11 +99,12 @@ constexpr int kThreads = 512;
 // What both kinds of wave know of an item.
 struct Shared {
     uint8_t *kv, *p;                   // [kRing] steps of keys; [2] steps of probabilities
+    uint8_t *raw;                      // of an 8-bit cache: [4 waves][2] shares of steps on their way
     float *red, *fac, *sum;            // [2][2][64] maxima by step parity and key half; [64]; [2][64]
     int *raise, *bad;                  // [3] by step; one flag
     int t0, t1, open;                  // steps; keys below `open` are seen by every row
     template <bool Q8>
-    __device__ uint8_t *ring(int t) const { return kv + ((t - t0) & (kRing - 1)) * kStepBytes<Q8>; }
+    __device__ uint8_t *ring(int t) const { return kv + (Q8 ? (t - t0) % kRing<Q8> : (t - t0) & (kRing<Q8> - 1)) * kStepBytes; }
     __device__ uint8_t *weights(int t) const { return p + (t & 1) * (kTileRows * 64); }
     __device__ float *maxima(int t, int half) const { return red + ((t & 1) * 2 + half) * kTileRows; }
 };
@@ -113,7 +117,7 @@ template <bool BF, bool Q8>
 __device__ __forceinline__ void clean(const Shared &sh, int t) {
     dev::lds_barrier();                                  // every wave has read the step's keys; the copies in flight are of other steps
     u32x4 *v = reinterpret_cast<u32x4 *>(sh.ring<Q8>(t));
-    for (int i = threadIdx.x; i < kLatentBlocks * kBlockBytes<Q8> / 16; i += kThreads) {
+    for (int i = threadIdx.x; i < kLatentBlocks * kBlockBytes / 16; i += kThreads) {
         u32x4 w = v[i];
 #pragma unroll
         for (int d = 0; d < 4; ++d) w[d] &= ~dev::nonfinite_halves<BF>(w[d]);
@@ -122,99 +126,121 @@ __device__ __forceinline__ void clean(const Shared &sh, int t) {
     dev::lds_barrier();
 }
 
-// A wave's share of the steps of an 8-bit cache: of each step keys 4 wave .. + 3, loaded
-// two steps before they are written to LDS as the 16-bit values that they stand for,
-// so that the products are those of a 16-bit cache.  (Every stored value is one of
-// the 16-bit type: the scales are powers of two within its range.)  Lane L holds 16
-// values of keys L / 32 and 2 + L / 32 from value 16 (L % 32) on, their scales, and of
-// the lower 32 lanes each 8 rotary values of key L / 8.
-struct Stage {
-    u32x4 q[2], pe;
-    uint32_t by[2];
-};
-template <bool BF, bool ONCE>
+// A summing wave's share of an 8-bit cache's steps: of each step keys 8 wave .. + 7, whose
+// bytes it copies into LDS two steps ahead, as they lie in memory, and then writes into
+// the ring as the 16-bit values that they stand for: the scoring waves work as on a
+// 16-bit cache.  (Every stored value is one of the 16-bit type: the scales are powers of
+// two within its range.)  A wave waits for its own copies alone.
+template <bool ONCE>
 struct Source8 {
-    const uint8_t *base;
+    static constexpr int kUnits = kRow8Bytes / 16, kKeys = 8, kCopies = (kKeys * kUnits + 63) / 64;
+    const uint8_t *base, *raw;
     const int32_t *table;
     int64_t page_bytes;
-    int shift, cols, n_pages, len, last, key0;
+    uint32_t raw_lds;
+    int shift, cols, n_pages, len, t0, last, key0;
     bool bad = false;
-    int page;                          // of the step that is loaded next, where it is the wave's
+    int page = 0;                      // of the keys of the step that is copied next
+    // Of a step between its wait and its writing.
+    u32x2 q[8];
+    u32x4 pe;
+    uint32_t by;
 
-    __device__ __forceinline__ Source8(const DecodeArgs &a, const DecodeItem &it, const Shared &sh)
-        : base(a.cache.base), table(a.cache.table + it.seq * a.cache.table_stride), page_bytes(a.cache.page_bytes), shift(a.cache.page_shift),
-          cols(a.cache.table_cols), n_pages(a.cache.n_pages), len(it.len), last(sh.t1 - 1), key0(4 * dev::wave_id()) {}
-    // Pages of four rows or more hold all of a wave's keys of a step: the number is then
-    // read by the scalar unit, a step ahead.
-    __device__ __forceinline__ void ask(int t) {
-        const int pos = min(min(t, last) * kStepKeys + key0, len - 1);
-        page = dev::ld_uniform(table + min(pos >> shift, max(cols, 1) - 1));
+    __device__ __forceinline__ Source8(const DecodeArgs &a, const DecodeItem &it, const Shared &sh, uint32_t lds)
+        : base(a.cache.base), raw(sh.raw + (dev::wave_id() & 3) * 2 * kRawBytes), table(a.cache.table + it.seq * a.cache.table_stride),
+          page_bytes(a.cache.page_bytes), raw_lds(lds + (dev::wave_id() & 3) * 2 * kRawBytes), shift(a.cache.page_shift), cols(a.cache.table_cols),
+          n_pages(a.cache.n_pages), len(it.len), t0(sh.t0), last(sh.t1 - 1), key0(kKeys * (dev::wave_id() & 3)) {}
+    // Past the end the last step is copied again, and keys past the last one are that one.
+    __device__ __forceinline__ int position(int t) const { return min(min(t, last) * kStepKeys + key0, len - 1); }
+    // Pages of eight rows or more hold all of the wave's keys; their number is read by the
+    // scalar unit a step ahead.
+    __device__ __forceinline__ void ask(int t) { page = dev::ld_uniform(table + min(position(t) >> shift, max(cols, 1) - 1)); }
+    __device__ __forceinline__ const uint8_t *row_at(int pos, int page) {
+        const bool off = page < 0 || page >= n_pages || pos >> shift >= cols;
+        bad = bad || off;
+        return base + (off ? 0 : page) * page_bytes + (pos & ((1 << shift) - 1)) * kRow8Bytes;
     }
-    __device__ __forceinline__ const uint8_t *row(int t, int k) {
-        const int pos = min(min(t, last) * kStepKeys + key0 + k, len - 1), at = pos >> shift;
-        int p = shift >= 2 ? page : table[min(at, max(cols, 1) - 1)];
-        if (p < 0 || p >= n_pages || at >= cols) {
-            bad = true;
-            p = 0;
-        }
-        return base + p * page_bytes + (pos & ((1 << shift) - 1)) * kRow8Bytes;
+    static __device__ __forceinline__ void copy16(const uint8_t *src, uint32_t dst) {
+        if constexpr (ONCE) dev::copy16_to_lds_once(src, dst);
+        else dev::copy16_to_lds_free(src, dst);
     }
-    static __device__ __forceinline__ u32x4 load16(const uint8_t *p) {
-        const __attribute__((address_space(1))) u32x4 *g = (const __attribute__((address_space(1))) u32x4 *)p;
-        if constexpr (ONCE) return __builtin_nontemporal_load(g);
-        else return *g;
-    }
-    __device__ __forceinline__ void load(Stage &s, int t) {
-        const int lane = threadIdx.x & 63, c = lane & 31;
+    __device__ __forceinline__ void copy(int t) {
+        const int lane = threadIdx.x & 63, pos = position(t), most = len - 1 - pos;
+        const uint32_t dst = raw_lds + ((t - t0) & 1) * kRawBytes;
+        if (shift >= 3 && most >= kKeys - 1) {
+            const uint8_t *r = row_at(pos, page) + 16 * lane;
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const uint8_t *r = row(t, 2 * j + (lane >> 5));
-            s.q[j] = load16(r + 16 * c);
-            s.by[j] = *(const __attribute__((address_space(1))) uint8_t *)(r + kRow8Scales + (c >> 1));
+            for (int i = 0; i < kKeys * kUnits / 64; ++i) copy16(r + 1024 * i, dst + 1024 * i);
+            if (lane < kKeys * kUnits % 64) copy16(r + 1024 * (kCopies - 1), dst + 1024 * (kCopies - 1));
+        } else {
+            // The last keys, or small pages: each lane finds its key's row.  (Vector loads of
+            // the table wait for the copies in flight, no more.)
+#pragma unroll 1
+            for (int i = 0; i < kCopies; ++i) {
+                const int u = 64 * i + lane, k = u / kUnits, p = pos + min(k, most), at = p >> shift;
+                if (u < kKeys * kUnits) {
+                    int page = table[min(at, max(cols, 1) - 1)];
+                    asm volatile("" : "+v"(page));
+                    const bool off = page < 0 || page >= n_pages || at >= cols;
+                    bad = bad || off;
+                    copy16(base + (off ? 0 : page) * page_bytes + (p & ((1 << shift) - 1)) * kRow8Bytes + 16 * (u - k * kUnits), dst + 1024 * i);
+                }
+            }
         }
-        if (lane < 32) s.pe = load16(row(t, lane >> 3) + kRow8Rope + 16 * (lane & 7));
-        ask(t + 1);
     }
-    __device__ __forceinline__ void store_latent(const Stage &s, uint8_t *place, int j) const {
-        const int lane = threadIdx.x & 63, c = lane & 31, r = key0 + 2 * j + (lane >> 5);
-        const float by = __uint_as_float(s.by[j] << 23);
+    // Step t into registers, and step t + 2 on its way in its place.  Lane L holds 64 values
+    // of key L / 8, 16 of each 128 columns from 16 (L % 8) on, the scales' bytes, and 8 rotary
+    // values.  Of 16 values the upper four lanes of a key take the upper half first:
+    // they lie in the same places of another block, and are written at the same time.
+    __device__ __forceinline__ void fetch(int t) {
+        const int lane = threadIdx.x & 63, c = lane & 7;
+        const uint8_t *from = raw + ((t - t0) & 1) * kRawBytes + (lane >> 3) * kRow8Bytes;
+        asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kCopies) : "memory");
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-            *reinterpret_cast<u32x4 *>(place + (c >> 2) * kBlockBytes<true> + dev::tile_unit(r, 2 * (c & 3) + i)) =
-                u32x4{dev::of_fp8<BF, false>(s.q[j][2 * i], by), dev::of_fp8<BF, true>(s.q[j][2 * i], by),
-                      dev::of_fp8<BF, false>(s.q[j][2 * i + 1], by), dev::of_fp8<BF, true>(s.q[j][2 * i + 1], by)};
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) q[2 * j + h] = *reinterpret_cast<const u32x2 *>(from + 128 * j + 16 * c + 8 * (h ^ (c >> 2)));
+        by = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) by |= static_cast<uint32_t>(from[kRow8Scales + 4 * j + (c >> 1)]) << (8 * j);
+        pe = *reinterpret_cast<const u32x4 *>(from + kRow8Rope + 16 * c);
     }
-    __device__ __forceinline__ void store_rope(const Stage &s, uint8_t *place) const {
-        const int lane = threadIdx.x & 63;
-        if (lane < 32) *reinterpret_cast<u32x4 *>(place + kLatentBlocks * kBlockBytes<true> + dev::tile_unit(key0 + (lane >> 3), lane & 7)) = s.pe;
+    __device__ __forceinline__ void copy_next(int t) {
+        asm volatile("s_waitcnt lgkmcnt(0)" : "+v"(q[0]), "+v"(q[1]), "+v"(q[2]), "+v"(q[3]), "+v"(q[4]), "+v"(q[5]), "+v"(q[6]), "+v"(q[7]), "+v"(pe), "+v"(by)::"memory");
+        copy(t + 2);
     }
-    __device__ __forceinline__ void store(const Stage &s, uint8_t *place) const {
-        store_latent(s, place, 0);
-        store_latent(s, place, 1);
-        store_rope(s, place);
+    template <bool BF>
+    __device__ __forceinline__ void write(uint8_t *place, int j) const {
+        const int lane = threadIdx.x & 63, c = lane & 7, r = key0 + (lane >> 3);
+        const float f = __uint_as_float(j == 0 ? by << 23 : by >> (8 * j) << 23);   // of a scale the conversion sees the exponent bits alone
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            *reinterpret_cast<u32x4 *>(place + (2 * j + (c >> 2)) * kBlockBytes + dev::tile_unit(r, 2 * (c & 3) + (h ^ (c >> 2)))) =
+                u32x4{dev::of_fp8<BF, false>(q[2 * j + h][0], f), dev::of_fp8<BF, true>(q[2 * j + h][0], f), dev::of_fp8<BF, false>(q[2 * j + h][1], f),
+                      dev::of_fp8<BF, true>(q[2 * j + h][1], f)};
+        if (j == 3) *reinterpret_cast<u32x4 *>(place + kLatentBlocks * kBlockBytes + dev::tile_unit(r, c)) = pe;
+    }
+    template <bool BF>
+    __device__ __forceinline__ void pass_on(int t, uint8_t *place) {
+        fetch(t);
+        copy_next(t);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) write<BF>(place, j);
     }
 };
 
 // The scoring waves' part of an item: wave (wm, wk) scores keys 16 wk .. + 15 of
 // each step for rows 32 wm .. + 31; lane L owns rows row and row + 16, row =
 // 32 wm + L % 16.  Leaves the running maxima in m.
-template <bool BF, bool ONCE, bool Q8>
+template <bool BF, bool Q8>
 __device__ __forceinline__ void score_item(const DecodeArgs &a, const DecodeItem &it, const Shared &sh, int rows, bool careful,
-                                           bool &bad_page, float (&m)[2]) {
+                                           float (&m)[2]) {
     const int lane = threadIdx.x & 63, wave = dev::wave_id();
     const int wm = wave & 1, wk = (wave >> 1) & 1, l15 = lane & 15, lq = lane >> 4;
     const int row = 32 * wm + l15;
     const float c = a.scale * kLog2e;
     int node[2];
     u32x4 q[kDepth][2];
-    Stage st[2];                                         // of an 8-bit cache: steps t0 and t0 + 1, later t + 1 and t + 2
-    Source8<BF, ONCE> src(a, it, sh);
-    if constexpr (Q8)
-        if (sh.t0 < sh.t1) {
-            src.ask(sh.t0);
-            src.load(st[0], sh.t0);
-            src.load(st[1], sh.t0 + 1);
-        }
 #pragma unroll
     for (int rb = 0; rb < 2; ++rb) node[rb] = (it.row0 + min(row + 16 * rb, rows - 1)) / a.n_heads;
     if (sh.t0 < sh.t1) {
@@ -223,7 +249,7 @@ __device__ __forceinline__ void score_item(const DecodeArgs &a, const DecodeItem
         // its products take them, they let the first step begin 11400 clocks after
         // the item, so 3900 (one token, 4096 keys 19.9 -> 16.9 us).
         const int r = 8 * wave + (lane >> 3), unit = ((lane & 7) ^ dev::tile_swz(r)) << 4;
-        const uint32_t at = dev::lds_address(sh.kv) + 2 * kStepBytes<Q8> + wave * 1024;
+        const uint32_t at = dev::lds_address(sh.kv) + (kRing<Q8> - 2) * kStepBytes + wave * 1024;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const int rr = it.row0 + min(r + 32 * h, rows - 1), n = rr / a.n_heads, head = rr - n * a.n_heads;
@@ -232,25 +258,28 @@ __device__ __forceinline__ void score_item(const DecodeArgs &a, const DecodeItem
             const uint8_t *qp = a.q_pe + (tok * a.qp_tok + head * a.qp_head) * 2 + unit;
 #pragma unroll
             for (int b = 0; b < kBlocks; ++b)
-                dev::copy16_to_lds_free(b < kLatentBlocks ? ql + 128 * b : qp, at + h * kStepBytes<Q8> + b * kBlockBytes<Q8>);
+                dev::copy16_to_lds_free(b < kLatentBlocks ? ql + 128 * b : qp, at + h * kStepBytes + b * kBlockBytes);
         }
         dev::copy_barrier();
-        const uint8_t *mine = sh.kv + (2 + wm) * kStepBytes<Q8>;
+        const uint8_t *mine = sh.kv + (kRing<Q8> - 2 + wm) * kStepBytes;
 #pragma unroll
         for (int k = 0; k < kDepth; ++k)
 #pragma unroll
             for (int rb = 0; rb < 2; ++rb)
-                q[k][rb] = *reinterpret_cast<const u32x4 *>(mine + (k >> 1) * kBlockBytes<Q8> + dev::tile_unit(l15 + 16 * rb, 4 * (k & 1) + lq));
+                q[k][rb] = *reinterpret_cast<const u32x4 *>(mine + (k >> 1) * kBlockBytes + dev::tile_unit(l15 + 16 * rb, 4 * (k & 1) + lq));
     }
     __builtin_amdgcn_s_setprio(2);   // the step waits for these waves: the summing ones fill what they leave
     m[0] = m[1] = -__builtin_inff();
     float l[2] = {0.0f, 0.0f};
-    f32x4 s[2], s_prev[2];
-    float sum_prev[2];
+    f32x4 s[2] = {}, s_prev[2] = {};
+    float sum_prev[2] = {0.0f, 0.0f};
+    // With 32 rows or fewer two of the waves have none, and only keep up with the barriers.
+    const bool idle = 32 * wm >= rows;
     auto score = [&](int t) {
+        if (idle) return;
         const uint8_t *kr = sh.ring<Q8>(t) + 16 * wk * 128;
         auto key = [&](int k) {
-            return *reinterpret_cast<const u32x4 *>(kr + (k >> 1) * kBlockBytes<Q8> + dev::tile_unit(l15, 4 * (k & 1) + lq));
+            return *reinterpret_cast<const u32x4 *>(kr + (k >> 1) * kBlockBytes + dev::tile_unit(l15, 4 * (k & 1) + lq));
         };
         u32x4 kf[kKeyAhead];
 #pragma unroll
@@ -296,6 +325,7 @@ __device__ __forceinline__ void score_item(const DecodeArgs &a, const DecodeItem
     // Probabilities of scores v against the running maxima; the lane's part of
     // the row sums.
     auto weigh = [&](int t, const f32x4 (&v)[2], float (&sum)[2]) {
+        if (idle) return;
 #pragma unroll
         for (int rb = 0; rb < 2; ++rb) {
             float p[4];
@@ -336,25 +366,17 @@ __device__ __forceinline__ void score_item(const DecodeArgs &a, const DecodeItem
         l[1] += sum_prev[1];
         if (careful && (t + 1) * kStepKeys > sh.open) clean<BF, Q8>(sh, t);
     };
-    // Step t + 1 of an 8-bit cache into LDS; its place is asked for step t + 3.
-    auto pass_on = [&](Stage &from, int t) {
-        src.store(from, sh.ring<Q8>(t + 1));
-        src.load(from, t + 3);
-    };
-
     if (sh.t0 < sh.t1) {
         // First step: its maxima are exchanged before it is weighed.
-        if constexpr (Q8) pass_on(st[0], sh.t0 - 1);
         dev::lds_barrier();
         score(sh.t0);
         post_max(sh.t0, s);
-        if constexpr (Q8) pass_on(st[1], sh.t0);
         dev::lds_barrier();
         take_max(sh.t0, 0.0f);
         weigh(sh.t0, s, sum_prev);
         s_prev[0] = s[0];
         s_prev[1] = s[1];
-        auto step = [&](int t, Stage &from) {
+        for (int t = sh.t0 + 1; t < sh.t1; ++t) {
             dev::lds_barrier();
             const int raise = sh.raise[(t - 1 - sh.t0) % 3];
             if (threadIdx.x == 0) sh.raise[(t + 1 - sh.t0) % 3] = 0;
@@ -364,17 +386,6 @@ __device__ __forceinline__ void score_item(const DecodeArgs &a, const DecodeItem
             if (__any(lane_max(s[0]) > limit[0] || lane_max(s[1]) > limit[1])) sh.raise[(t - sh.t0) % 3] = 1;
             s_prev[0] = s[0];
             s_prev[1] = s[1];
-            if constexpr (Q8) pass_on(from, t);
-        };
-        if constexpr (Q8) {                              // two steps a turn: what is in flight stays in its registers
-            int t = sh.t0 + 1;
-            for (; t + 1 < sh.t1; t += 2) {
-                step(t, st[0]);
-                step(t + 1, st[1]);
-            }
-            if (t < sh.t1) step(t, st[0]);
-        } else {
-            for (int t = sh.t0 + 1; t < sh.t1; ++t) step(t, st[0]);
         }
         dev::lds_barrier();
         settle(sh.t1 - 1, sh.raise[(sh.t1 - 1 - sh.t0) % 3]);
@@ -384,13 +395,12 @@ __device__ __forceinline__ void score_item(const DecodeArgs &a, const DecodeItem
         const float sum = dev::sum_halves(dev::sum_quarters(l[rb]));
         if (lq == 0) sh.sum[wk * kTileRows + row + 16 * rb] = sum;
     }
-    if constexpr (Q8) bad_page = bad_page || src.bad;
 }
 
 // The summing waves' part: wave w copies keys 8 w .. + 7 of each step and sums
 // columns 128 w .. + 127 for all rows.
 template <bool BF, bool ONCE, bool Q8>
-__device__ __forceinline__ void sum_item(const DecodeArgs &a, const DecodeItem &it, const Shared &sh, uint32_t kv_lds, bool careful,
+__device__ __forceinline__ void sum_item(const DecodeArgs &a, const DecodeItem &it, const Shared &sh, uint32_t kv_lds, uint32_t raw_lds, int rows, bool careful,
                                          bool &bad_page, f32x16 (&acc)[4][2]) {
     const int lane = threadIdx.x & 63, wave = dev::wave_id() & 3, l31 = lane & 31, lh = lane >> 5;
 #pragma unroll
@@ -430,11 +440,11 @@ __device__ __forceinline__ void sum_item(const DecodeArgs &a, const DecodeItem &
             page = 0;
         }
         return Copy{a.cache.base + page * a.cache.page_bytes + (pos & ((1 << shift) - 1)) * kRowBytes + cu,
-                    kv_lds + ((t - sh.t0) & (kRing - 1)) * kStepBytes<Q8> + wave * 1024};
+                    kv_lds + ((t - sh.t0) & (kRing<false> - 1)) * kStepBytes + wave * 1024};
     };
     auto copy = [&](const Copy &x, int b) {
-        if constexpr (ONCE) dev::copy16_to_lds_once(x.src + b * 128, x.dst + b * kBlockBytes<Q8>);
-        else dev::copy16_to_lds_free(x.src + b * 128, x.dst + b * kBlockBytes<Q8>);
+        if constexpr (ONCE) dev::copy16_to_lds_once(x.src + b * 128, x.dst + b * kBlockBytes);
+        else dev::copy16_to_lds_free(x.src + b * 128, x.dst + b * kBlockBytes);
     };
     auto copy_all = [&](const Copy &x) {
 #pragma unroll
@@ -445,10 +455,10 @@ __device__ __forceinline__ void sum_item(const DecodeArgs &a, const DecodeItem &
     // waves' copies keep the CU's address unit busy for about 900 clocks, nearly
     // as long as both kinds' products take.
     const int kr0 = 8 * lh + ((lane >> 2) & 3);
-    Source8<BF, ONCE> src(a, it, sh);
-    auto step = [&](int t, bool more, Copy &now, int &page, Stage &from) {
+    Source8<ONCE> src(a, it, sh, raw_lds);
+    auto step = [&](int t, bool more, Copy &now, int &page) {
         const int raise = sh.raise[(t - sh.t0) % 3];
-        const uint8_t *vr = sh.ring<Q8>(t) + 2 * wave * kBlockBytes<Q8> + 8 * (lane & 1);
+        const uint8_t *vr = sh.ring<Q8>(t) + 2 * wave * kBlockBytes + 8 * (lane & 1);
         const uint8_t *pr = sh.weights(t);
         u32x4 pf[2][2], vf[2][4];
         auto read_weights = [&]() {
@@ -462,7 +472,7 @@ __device__ __forceinline__ void sum_item(const DecodeArgs &a, const DecodeItem &
             for (int k = 0; k < 2; ++k)
 #pragma unroll
                 for (int cb = 0; cb < 4; ++cb) {
-                    const uint8_t *blk = vr + (cb >> 1) * kBlockBytes<Q8> + 16 * k * 128;
+                    const uint8_t *blk = vr + (cb >> 1) * kBlockBytes + 16 * k * 128;
                     const int unit = 4 * (cb & 1) + 2 * ((lane >> 4) & 1) + ((lane >> 1) & 1);
                     const u32x2 a0 = dev::read_tr(blk + dev::tile_unit(kr0, unit));
                     const u32x2 a1 = dev::read_tr(blk + dev::tile_unit(kr0 + 4, unit));
@@ -490,7 +500,7 @@ __device__ __forceinline__ void sum_item(const DecodeArgs &a, const DecodeItem &
             read_values();
         }
         Copy next = now;
-        uint8_t *place = sh.ring<Q8>(t + 2);
+        if (Q8 && more) src.ask(t + 4);
         if (!Q8 && more) copy(now, 0);
 #pragma unroll
         for (int k = 0; k < 2; ++k)
@@ -498,15 +508,13 @@ __device__ __forceinline__ void sum_item(const DecodeArgs &a, const DecodeItem &
             for (int cb = 0; cb < 4; ++cb) {
                 __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                for (int rb = 0; rb < 2; ++rb) acc[cb][rb] = dev::mma<BF>(vf[k][cb], pf[k][rb], acc[cb][rb]);
+                for (int rb = 0; rb < 2; ++rb)
+                    if (rb == 0 || rows > 32) acc[cb][rb] = dev::mma<BF>(vf[k][cb], pf[k][rb], acc[cb][rb]);
                 __builtin_amdgcn_sched_barrier(0);
                 if constexpr (Q8) {
-                    if (more && k == 0 && cb == 0) src.store_latent(from, place, 0);
-                    if (more && k == 0 && cb == 2) src.store_latent(from, place, 1);
-                    if (more && k == 1 && cb == 0) {
-                        src.store_rope(from, place);
-                        src.load(from, t + 4);
-                    }
+                    if (more && k == 0 && cb == 0) src.fetch(t + 2);
+                    if (more && k == 0 && cb == 2) src.copy_next(t + 2);
+                    if (more && k == 1) src.template write<BF>(sh.ring<Q8>(t + 2), cb);
                 } else {
                     if (more) copy(now, 1 + 4 * k + cb);
                     if (more && k == 1 && cb == 1) {
@@ -518,32 +526,25 @@ __device__ __forceinline__ void sum_item(const DecodeArgs &a, const DecodeItem &
         now = next;
     };
 
-    Stage st[2];
     Copy now{};
     int page = 0;
     if constexpr (Q8) {
         src.ask(sh.t0);
-        src.load(st[0], sh.t0);
-        src.load(st[1], sh.t0 + 1);
+        src.copy(sh.t0);
+        src.ask(sh.t0 + 1);
+        src.copy(sh.t0 + 1);
+        src.ask(sh.t0 + 2);
         dev::lds_barrier();                              // the queries have landed
-        src.store(st[0], sh.ring<Q8>(sh.t0));
-        src.load(st[0], sh.t0 + 2);
+        src.template pass_on<BF>(sh.t0, sh.ring<Q8>(sh.t0));
+        src.ask(sh.t0 + 3);
         dev::lds_barrier();                              // step t0 has been written, and the queries have been read
-        src.store(st[1], sh.ring<Q8>(sh.t0 + 1));
-        src.load(st[1], sh.t0 + 3);
+        src.template pass_on<BF>(sh.t0 + 1, sh.ring<Q8>(sh.t0 + 1));
         dev::lds_barrier();                              // the first maxima
-        int t = sh.t0 + 1;
-        for (; t + 1 < sh.t1; t += 2) {
+        for (int t = sh.t0 + 1; t < sh.t1; ++t) {
             dev::lds_barrier();
-            step(t - 1, true, now, page, st[0]);
-            dev::lds_barrier();
-            step(t, true, now, page, st[1]);
+            step(t - 1, true, now, page);
         }
-        if (t < sh.t1) {
-            dev::lds_barrier();
-            step(t - 1, true, now, page, st[0]);
-        }
-        dev::lds_barrier();
+        dev::copy_barrier();                             // what was copied past the end has landed too
         bad_page = bad_page || src.bad;
     } else {
         const int pg0 = page_of(sh.t0), pg1 = page_of(sh.t0 + 1), pg2 = page_of(sh.t0 + 2), pg3 = page_of(sh.t0 + 3);
@@ -561,11 +562,11 @@ __device__ __forceinline__ void sum_item(const DecodeArgs &a, const DecodeItem &
             // Step t has landed when only the copies of step t + 1 are in flight.
             asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kBlocks) : "memory");
             dev::lds_barrier();
-            step(t - 1, true, now, page, st[0]);
+            step(t - 1, true, now, page);
         }
         dev::copy_barrier();
     }
-    step(last, false, now, page, st[0]);
+    step(last, false, now, page);
     float z = 0.0f;
 #pragma unroll
     for (int cb = 0; cb < 4; ++cb)
@@ -668,8 +669,7 @@ __device__ __forceinline__ DecodeItem take_item(const DecodeArgs &a, int round, 
 
 template <bool BF, bool ONCE, bool Q8>
 __global__ __launch_bounds__(kThreads, 2) void latent_decode_kernel(DecodeArgs a) {
-    __shared__ __align__(1024) uint8_t s_kv[kRing * kStepBytes<Q8>];
-    __shared__ __align__(1024) uint8_t s_p[2 * kTileRows * 64];
+    __shared__ __align__(1024) uint8_t s_kv[kKeyBytes<Q8> + kWeightBytes + (Q8 ? 8 * kRawBytes : 0)];
     __shared__ float s_red[2 * 2 * kTileRows], s_fac[kTileRows], s_sum[2 * kTileRows];
     __shared__ int s_raise[3], s_bad;
     const int tid = threadIdx.x, lane = tid & 63, wave = dev::wave_id();
@@ -679,7 +679,7 @@ __global__ __launch_bounds__(kThreads, 2) void latent_decode_kernel(DecodeArgs a
     // The two kinds walk the items in loops of their own (and meet at the same
     // barriers): neither then holds registers for the other.
     bool more = true, bad_page = false;
-    Shared sh{s_kv, s_p, s_red, s_fac, s_sum, s_raise, &s_bad, 0, 0, 0};
+    Shared sh{s_kv, s_kv + kKeyBytes<Q8>, s_kv + kKeyBytes<Q8> + kWeightBytes, s_red, s_fac, s_sum, s_raise, &s_bad, 0, 0, 0};
     if (wave < 4) {
         for (int round = 0; more; ++round) {
             const DecodeItem it = take_item(a, round, more, sh);
@@ -689,7 +689,7 @@ __global__ __launch_bounds__(kThreads, 2) void latent_decode_kernel(DecodeArgs a
             for (int careful = 0; careful < 2; ++careful) {
                 dev::lds_barrier();                      // the buffers of the item (or pass) before are free
                 if (tid == 0) s_bad = s_raise[0] = s_raise[1] = s_raise[2] = 0;
-                score_item<BF, ONCE, Q8>(a, it, sh, rows, careful, bad_page, m);
+                score_item<BF, Q8>(a, it, sh, rows, careful, m);
                 dev::lds_barrier();
                 if (!(s_bad && sh.t1 * kStepKeys > sh.open)) break;
             }
@@ -718,7 +718,7 @@ __global__ __launch_bounds__(kThreads, 2) void latent_decode_kernel(DecodeArgs a
             f32x16 acc[4][2];                            // [32 columns][32 rows] blocks of O^T
             for (int careful = 0; careful < 2; ++careful) {
                 dev::lds_barrier();
-                sum_item<BF, ONCE, Q8>(a, it, sh, kv_lds, careful, bad_page, acc);
+                sum_item<BF, ONCE, Q8>(a, it, sh, kv_lds, kv_lds + kKeyBytes<Q8> + kWeightBytes, rows, careful, bad_page, acc);
                 if (careful) spoil_seen<BF, Q8>(a, it, sh, rows, acc);
                 dev::lds_barrier();
                 if (!(s_bad && sh.t1 * kStepKeys > sh.open)) break;
@@ -771,7 +771,9 @@ __global__ __launch_bounds__(256) void join_kernel(DecodeArgs a) {
     const int per = apart ? kOutBlocks / 4 : kOutBlocks;
     const int lane = threadIdx.x & 63, wave = dev::wave_id();
     for (int wg = blockIdx.x; wg < joins * per; wg += gridDim.x) {
-        const JoinUnit u = a.plan.joins[wg / per];
+        JoinUnit u = a.plan.joins[wg / per];
+        const bool group = u.split & kJoinGroup;
+        u.split &= ~kJoinGroup;
         const int block = apart ? 4 * (wg % per) + wave : wg % per;
         const int r = 32 * (block & 1) + (lane & 31);
         const bool live = r < u.rows;                     // partial rows past the unit's hold no statistics
@@ -780,38 +782,45 @@ __global__ __launch_bounds__(256) void join_kernel(DecodeArgs a) {
         float top = -__builtin_inff();
 #pragma unroll 8
         for (int i = 0; i < u.split; ++i) top = fmaxf(top, ml[i * kTileRows * 2]);
-        // Pieces of the group's prefix: the row lies elsewhere in the group's units.
-        const float *pml = nullptr;
-        const f32x4 *ppart = nullptr;
-        if (u.prefix_split) {
-            const int at = u.prefix_row + (live ? r : 0), pr = at % kTileRows;
-            const int64_t slot = u.prefix_slot0 + at / kTileRows * u.prefix_split;
-            pml = a.part_ml + (slot * kTileRows + pr) * 2;
-            ppart = reinterpret_cast<const f32x4 *>(a.part + slot * kTileRows * kLatent) + ((block & ~1) | (pr >> 5)) * 256 + ((lane & 32) | (pr & 31));
-#pragma unroll 8
-            for (int i = 0; i < u.prefix_split; ++i) top = fmaxf(top, pml[i * kTileRows * 2]);
+        // A group's rows: the pieces above are the prefix's, and each row has others, of its
+        // own sequence, somewhere in that one's units.
+        const float *oml = nullptr;
+        const f32x4 *opart = nullptr;
+        int own = 0, own_most = 0;
+        if (group) {
+            const int at = u.out_row + (live ? r : 0);
+            const int4v rec = *reinterpret_cast<const int4v *>(a.plan.records + at / a.n_heads);
+            const int in_seq = at - rec[2], orow = in_seq % kTileRows;
+            const int64_t slot = rec[0] + in_seq / kTileRows * rec[1];
+            own = rec[1];
+            oml = a.part_ml + (slot * kTileRows + orow) * 2;
+            opart = reinterpret_cast<const f32x4 *>(a.part + slot * kTileRows * kLatent) + ((block & ~1) | (orow >> 5)) * 256 + ((lane & 32) | (orow & 31));
+            for (int i = 0; i < own; ++i) top = fmaxf(top, oml[i * kTileRows * 2]);
+            own_most = own;
+#pragma unroll
+            for (int o = 32; o; o >>= 1) own_most = max(own_most, __shfl_xor(own_most, o, 64));
         }
         const float ms = top == -__builtin_inff() ? 0.0f : top;
         float l = 0.0f;
         f32x16 o;
 #pragma unroll
         for (int i = 0; i < 16; ++i) o[i] = 0.0f;
-        auto add = [&](const float *ml, const f32x4 *part, int split) {
-            const int p0 = apart ? 0 : split * wave / 4, p1 = apart ? split : split * (wave + 1) / 4;
-#pragma unroll 4
-            for (int i = p0; i < p1; ++i) {
-                const float f = __builtin_amdgcn_exp2f(ml[i * kTileRows * 2] - ms);
-                l = __builtin_fmaf(f, ml[i * kTileRows * 2 + 1], l);
+        auto add = [&](const float *ml, const f32x4 *part, int i) {
+            const float f = __builtin_amdgcn_exp2f(ml[i * kTileRows * 2] - ms);
+            l = __builtin_fmaf(f, ml[i * kTileRows * 2 + 1], l);
 #pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    const f32x4 v = part[static_cast<int64_t>(i) * (kTileRows * kLatent / 4) + 64 * g];
+            for (int g = 0; g < 4; ++g) {
+                const f32x4 v = part[static_cast<int64_t>(i) * (kTileRows * kLatent / 4) + 64 * g];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) o[4 * g + j] = __builtin_fmaf(f, v[j], o[4 * g + j]);
-                }
+                for (int j = 0; j < 4; ++j) o[4 * g + j] = __builtin_fmaf(f, v[j], o[4 * g + j]);
             }
         };
-        add(ml, part, u.split);
-        if (u.prefix_split) add(pml, ppart, u.prefix_split);
+        // The four waves of a workgroup take a quarter each of all pieces, the own ones first.
+        const int all = own_most + u.split, p0 = apart ? 0 : all * wave / 4, p1 = apart ? all : all * (wave + 1) / 4;
+        for (int i = p0; i < min(p1, own_most); ++i)
+            if (i < own) add(oml, opart, i);
+#pragma unroll 4
+        for (int i = max(p0 - own_most, 0); i < p1 - own_most; ++i) add(ml, part, i);
         if (!apart) {
             __syncthreads();
             if (wave) {
@@ -899,15 +908,16 @@ __global__ __launch_bounds__(kPlanThreads) void decode_plan_kernel(DecodePlan p,
     int my_most = 1;
     // Of a sequence: its group (-1: none).  Of a group: first sequence and behind the
     // last, the least context of its tokens (later the tiles that it shares), how many
-    // of its sequences have tokens, and the first that does.
+    // of its sequences have tokens, the first that does, and the most pieces of one.
     __shared__ int s_group[PREFIX ? kSortMost : 1], s_from[PREFIX ? kSortMost + 1 : 1], s_least[PREFIX ? kSortMost : 1], s_live[PREFIX ? kSortMost : 1], s_head[PREFIX ? kSortMost : 1];
+    __shared__ int s_split[PREFIX ? kSortMost : 1];
     __shared__ int s_groups;
     const int q_seqs = n_seq;
     if constexpr (PREFIX) {
         if (tid == 0) s_groups = groups.n;
         if (tid <= groups.n) s_from[tid] = groups.start[tid];
         s_least[tid] = s_head[tid] = INT32_MAX;
-        s_live[tid] = 0;
+        s_live[tid] = s_split[tid] = 0;
         __syncthreads();
         if (tid < groups.n && (s_from[tid] < 0 || s_from[tid + 1] < s_from[tid] || s_from[tid + 1] > n_seq)) {
             bad = true;
@@ -1112,7 +1122,8 @@ __global__ __launch_bounds__(kPlanThreads) void decode_plan_kernel(DecodePlan p,
         int4 s = b >= n_seq ? int4{0, 0, 0, 0} : b < kSortMost ? s_seq[b] : seq[b];
         const int split = cut(s.y, best), count = s.x * split;
         const bool parts = b < n_seq && (split > 1 || shares(b));
-        const int units_joined = parts && (!PREFIX || b < q_seqs) ? s.x : 0;
+        // Rows of a group are joined in its units, those of other sequences in their own.
+        const int units_joined = parts && (!PREFIX || b >= q_seqs || s_at[b].w == 0) ? s.x : 0;
         int total;
         const int at = n_items + dev::block_exclusive_scan<kPlanThreads>(count, s_tmp, &total);
         n_items += total;
@@ -1126,26 +1137,20 @@ __global__ __launch_bounds__(kPlanThreads) void decode_plan_kernel(DecodePlan p,
             if (b < kSortMost) s_seq[b] = s;
             else seq[b] = s;
         }
-        if constexpr (PREFIX) __syncthreads();           // the groups' slots
+        if (PREFIX && parts && b < q_seqs && s_at[b].w > 0 && s.x) atomicMax(&s_split[s_group[b]], split);
+        if constexpr (PREFIX) __syncthreads();           // the groups' longest divisions
         if (units_joined) {
+            const bool group = PREFIX && b >= q_seqs;
             JoinUnit u{};
-            if constexpr (PREFIX)
-                if (shares(b)) {
-                    const int g = q_seqs + s_group[b];
-                    u.prefix_row = (s_at[b].x - s_at[g].x) * n_heads;
-                    u.prefix_slot0 = s_seq[g].w;
-                    u.prefix_split = cut(s_seq[g].y, best);
-                }
-            atomicMax(&s_most, split + u.prefix_split);
+            atomicMax(&s_most, split + (group ? s_split[b - q_seqs] : 0));
             if (slot + count <= p.slot_cap && join + s.x <= p.join_cap) {
                 const int q0 = b < kSortMost ? s_at[b].x : q_start[b], rows = (b < kSortMost ? s_at[b].y : q_start[b + 1] - q0) * n_heads;
-                u.split = split;
+                u.split = split | (group ? kJoinGroup : 0);
                 for (int i = 0; i < s.x; ++i) {
                     u.out_row = q0 * n_heads + i * kTileRows;
                     u.rows = min(kTileRows, rows - i * kTileRows);
                     u.slot0 = slot + i * split;
                     p.joins[join + i] = u;
-                    u.prefix_row += kTileRows;
                 }
             }
         }
@@ -1183,6 +1188,8 @@ __global__ __launch_bounds__(kPlanThreads) void decode_plan_kernel(DecodePlan p,
             const bool prefix = PREFIX && b >= q_seqs;
             const int behind = PREFIX && !prefix ? at.w : 0, seq_bits = prefix ? at.w | kItemPrefix : b;
             const int split = cut(s.y, best), each = s.y / split, over = s.y - each * split;
+            if (PREFIX && !prefix && behind)              // where the join finds the pieces of a token's rows
+                for (int i = tid % kItemLanes; i < at.y; i += kItemLanes) p.records[at.x + i] = int4v{s.w, split, at.x * n_heads, 0};
             // Neighbouring items: the units of one run of keys.
             for (int i = tid % kItemLanes; i < s.x * split; i += kItemLanes) {
                 const int c = i / s.x, u = i - c * s.x;

@@ -38,17 +38,21 @@ struct alignas(32) DecodeItem {
     int32_t row0, t0, t1, slot;
 };
 constexpr int32_t kItemMore = 1 << 30, kItemPrefix = 1 << 29;
-// Rows whose pieces are joined: `rows` output rows from out_row, the partials
-// slot0 .. slot0 + split - 1, and of the group's prefix: the unit's first row is row
-// prefix_row of the group, whose unit i has slots prefix_slot0 + i prefix_split ...
-struct alignas(32) JoinUnit {
+// Rows whose pieces are joined: `rows` output rows from out_row, the partials slot0 ..
+// slot0 + split - 1.  split | kJoinGroup: they are a group's and the partials those of its
+// prefix; each row has others, found by its token's record: of unit i of the sequence
+// whose first row is row0, slot0 + i split ...
+struct alignas(16) JoinUnit {
     int32_t out_row, rows, slot0, split;
-    int32_t prefix_row, prefix_slot0, prefix_split, unused;
 };
+constexpr int32_t kJoinGroup = 1 << 30;
+typedef int32_t TokenRecord __attribute__((ext_vector_type(4)));   // slot0, split, row0
+constexpr int kRecords = 65536;          // tokens of a plan with prefixes, whose rows (64 to a unit) have to find room
 struct DecodePlan {
     int32_t *head;             // [4] join units, the most pieces of one, tokens, sequences
     DecodeItem *items;
     JoinUnit *joins;
+    TokenRecord *records;      // [min(max_tokens, kRecords)]
     int32_t *seq;              // [max_seqs x 4] scratch of the planning
     int item_cap, join_cap, slot_cap;
 };

@@ -71,7 +71,7 @@ bool aligned(const void *p, size_t n) { return reinterpret_cast<uintptr_t>(p) % 
 constexpr int kSlotStats = 8;
 
 struct Sizes {
-    int64_t items, joins, slots, seqs;
+    int64_t items, joins, slots, seqs, records;
 };
 // Room of a plan: one item per 64-row unit (each sequence may end in a part of
 // one), and four rounds over the CUs of pieces; pieces of cut units hold
@@ -80,17 +80,18 @@ Sizes plan_sizes(const coli_serve_dims &d, int n_cu) {
     const int64_t units = static_cast<int64_t>(d.max_tokens) * d.n_heads / kTileRows + d.max_seqs;
     const int64_t slots = 4ll * n_cu;
     const int64_t rounds = (units + slots + n_cu - 1) / n_cu + 1;
-    return Sizes{rounds * n_cu, std::min(units, slots), slots, d.max_seqs};
+    return Sizes{rounds * n_cu, std::min(units, slots), slots, d.max_seqs, std::min(d.max_tokens, kRecords)};
 }
 size_t create_bytes(const coli_serve_dims &d, int n_cu) {
     const Sizes z = plan_sizes(d, n_cu);
     return static_cast<size_t>(z.items) * sizeof(DecodeItem) + static_cast<size_t>(z.joins) * sizeof(JoinUnit) +
+           static_cast<size_t>(z.records) * sizeof(TokenRecord) +
            static_cast<size_t>(z.slots) * kTileRows * (kLatent + kSlotStats) * sizeof(float) +
            static_cast<size_t>(z.seqs) * (8 * sizeof(int32_t) + 2 * sizeof(uint64_t) + sizeof(int32_t)) + 5 * sizeof(int32_t);
 }
 
 void free_serve(coli_serve *S) {
-    void *ptrs[] = {S->plan.head, S->plan.items, S->plan.joins, S->plan.seq, S->part, S->part_ml, S->walk, S->best, S->arrived, S->err};
+    void *ptrs[] = {S->plan.head, S->plan.items, S->plan.joins, S->plan.records, S->plan.seq, S->part, S->part_ml, S->walk, S->best, S->arrived, S->err};
     for (void *p : ptrs) book_free(p);
     delete S;
 }
@@ -217,7 +218,7 @@ coli_status make_plan(coli_serve *S, const int32_t *q_start, const int32_t *kv_l
     if (n_groups > 0) NEED(group_start && prefix_len, "NULL device pointer");
     // More sequences than a plan with prefixes handles could not share either: their
     // pieces would not find room.
-    if (n_seq + n_groups > kPrefixEntries) n_groups = 0;
+    if (n_seq + n_groups > kPrefixEntries || n_tok > kRecords) n_groups = 0;
     OnDevice on(S->device);
     CHECK(launched(S, launch_decode_plan(S->plan, q_start, kv_len, n_seq, n_tok, S->d.n_heads, S->n_cu, group_start, prefix_len, n_groups, S->err, static_cast<hipStream_t>(stream)),
                    "plan launch"));
@@ -309,6 +310,7 @@ coli_status coli_serve_create(const coli_serve_dims *d, int device, coli_serve *
         {reinterpret_cast<void **>(&S->plan.head), 4 * sizeof(int32_t), "plan head"},
         {reinterpret_cast<void **>(&S->plan.items), z.items * sizeof(DecodeItem), "plan items"},
         {reinterpret_cast<void **>(&S->plan.joins), z.joins * sizeof(JoinUnit), "plan joins"},
+        {reinterpret_cast<void **>(&S->plan.records), z.records * sizeof(TokenRecord), "plan records"},
         {reinterpret_cast<void **>(&S->plan.seq), z.seqs * 4 * sizeof(int32_t), "plan scratch"},
         {reinterpret_cast<void **>(&S->part), z.slots * kTileRows * kLatent * sizeof(float), "partial outputs"},
         {reinterpret_cast<void **>(&S->part_ml), z.slots * kTileRows * kSlotStats * sizeof(float), "partial statistics"},
