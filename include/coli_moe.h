@@ -581,7 +581,8 @@ coli_status coli_latent_read(coli_serve *serve, int32_t cache_kind, const void *
 
 /* Plan a step whose sequences come in groups that begin with the same tokens: group g
  * is sequences group_start[g] .. group_start[g + 1] - 1 (int32 [n_groups + 1],
- * ascending, within 0..n_seq; sequences of no group are planned as before), of which
+ * ascending, within 0..n_seq; sequences before the first group and behind the last are
+ * planned as before, and so are those of a group whose prefix_len is 0), of which
  * the first prefix_len[g] positions hold the same rows (on the same pages, or copies of
  * them; the call trusts that, and reads them through one sequence's row of the block
  * table).  The decode calls that follow give what they give after coli_latent_plan, up to
