@@ -24,7 +24,11 @@ namespace {
 constexpr int kThreads = 256, kWaves = kThreads / 64;
 constexpr int kCandidates = 1024;        // elements at or above the threshold that are ranked by counting
 constexpr int kJoinThreads = 512, kJoinCandidates = 2048;
+constexpr int kHeld = 8;                 // a thread's candidates that stay in registers
 constexpr float kLog2e = 1.44269504088896341f;
+
+// The smallest key of a candidate: of -FLT_MAX.
+constexpr uint32_t kLeastKey = 0x00800000u;
 
 // Values in the order of their keys: NaN counts as -inf, whose key is zero, no
 // candidate; -0 and +0 share a key.
@@ -34,7 +38,8 @@ __device__ __forceinline__ float value_of(uint32_t key) { return __uint_as_float
 __device__ __forceinline__ uint64_t packed(uint32_t key, uint32_t token) { return static_cast<uint64_t>(key) << 32 | (0xFFFFFFFFu - token); }
 
 // The largest key that `keep` lanes of the wave reach (0 where fewer than that have a
-// candidate), by its bits from the highest down.
+// candidate), by its bits from the highest down.  (A key that up to a quarter more lanes
+// reach is found sooner, but leaves more to rank: 256 rows of 151643 logits 49 us, so 44.)
 __device__ __forceinline__ uint32_t reached(uint32_t key, int keep) {
     uint32_t t = 0;
     for (int b = 31; b >= 0; --b) {
@@ -69,11 +74,11 @@ __global__ __launch_bounds__(kThreads) void select_kernel(SelectArgs a, int row0
         const int at = first + (j * kThreads + tid) * 4;
         if (at + 4 <= a.vocab) {
             if constexpr (KIND == COLI_PROB_F32) {
-                const f32x4u v = *reinterpret_cast<const f32x4u *>(z + 4ll * at);
+                const f32x4u v = __builtin_nontemporal_load(reinterpret_cast<const f32x4u *>(z + 4ll * at));
 #pragma unroll
                 for (int i = 0; i < 4; ++i) x[4 * j + i] = v[i];
             } else {
-                const u16x4u v = *reinterpret_cast<const u16x4u *>(z + 2ll * at);
+                const u16x4u v = __builtin_nontemporal_load(reinterpret_cast<const u16x4u *>(z + 2ll * at));
 #pragma unroll
                 for (int i = 0; i < 4; ++i) x[4 * j + i] = dev::lo16<KIND == COLI_PROB_BF16>(v[i]);
             }
@@ -92,20 +97,25 @@ __global__ __launch_bounds__(kThreads) void select_kernel(SelectArgs a, int row0
     if (tid == 0) s_count = 0;
     float most = -__builtin_inff();
 #pragma unroll
-    for (int e = 0; e < EACH; ++e) most = fmaxf(most, x[e]);          // a NaN is passed over
+    for (int e = 0; e < EACH; ++e) {
+        x[e] = fmaxf(x[e], -__builtin_inff());                        // NaN counts as -inf
+        most = fmaxf(most, x[e]);
+    }
     const uint32_t mine = key_of(most);
     float top = most;
 #pragma unroll
     for (int o = 32; o; o >>= 1) top = fmaxf(top, __shfl_xor(top, o, 64));
     float sum = 0.0f;
-    if (top > -__builtin_inff()) {
+    if (fabsf(top) < 0x1p100f) {
+        // 2^(z log2 e - top log2 e) by one multiply-add, rounded where it is small; the
+        // rounding of the product with top, the same for all, is taken back behind the sum.
+        const float c = top * kLog2e, left = __builtin_fmaf(top, kLog2e, -c);
 #pragma unroll
-        for (int e = 0; e < EACH; ++e) {
-            // z - top is taken first: it is exact for the terms that count, and its product
-            // with log2 e is off by half a unit of itself, which they keep small.
-            const float t = __builtin_amdgcn_exp2f((x[e] - top) * kLog2e);
-            sum += x[e] > -__builtin_inff() ? t : 0.0f;               // of a NaN: nothing
-        }
+        for (int e = 0; e < EACH; ++e) sum += __builtin_amdgcn_exp2f(__builtin_fmaf(x[e], kLog2e, -c));
+        sum *= __builtin_amdgcn_exp2f(-left);
+    } else if (top > -__builtin_inff()) {
+#pragma unroll
+        for (int e = 0; e < EACH; ++e) sum += __builtin_amdgcn_exp2f((x[e] - top) * kLog2e);
     }
 #pragma unroll
     for (int o = 32; o; o >>= 1) sum += __shfl_xor(sum, o, 64);
@@ -116,17 +126,27 @@ __global__ __launch_bounds__(kThreads) void select_kernel(SelectArgs a, int row0
         s_reach[wave] = reach;
     }
     __syncthreads();
-    uint32_t limit = 1;
+    uint32_t limit = kLeastKey;
 #pragma unroll
     for (int w = 0; w < kWaves; ++w) limit = max(limit, s_reach[w]);
     auto token_of = [&](int e) { return static_cast<uint32_t>(first + ((e >> 2) * kThreads + tid) * 4 + (e & 3)); };
-    if (mine >= limit) {
+    const float least = value_of(limit);
+    // The threshold is reached by few: a wave looks at one element of all lanes at a time,
+    // first to count them, so that it takes its places of the list at once.
+    int found = 0;
+#pragma unroll
+    for (int e = 0; e < EACH; ++e) found += __popcll(__ballot(x[e] >= least));
+    if (found) {
+        int to = 0;
+        if (lane == 0) to = atomicAdd(&s_count, found);
+        to = __builtin_amdgcn_readfirstlane(to);
 #pragma unroll
         for (int e = 0; e < EACH; ++e) {
-            const uint32_t key = key_of(x[e]);
-            if (key >= limit) {
-                const int at = atomicAdd(&s_count, 1);
-                if (at < kCandidates) s_cand[at] = packed(key, token_of(e));
+            const uint64_t m = __ballot(x[e] >= least);
+            if (m) {
+                const int at = to + __popcll(m & ((1ull << lane) - 1));
+                if (x[e] >= least && at < kCandidates) s_cand[at] = packed(key_of(x[e]), token_of(e));
+                to += __popcll(m);
             }
         }
     }
@@ -183,13 +203,13 @@ __global__ __launch_bounds__(kThreads) void select_kernel(SelectArgs a, int row0
     }
 }
 
-// A candidate's place: by score, then by beam and token.
+// A candidate's place: by score, then by beam and token, which `id` holds one above the
+// other.  (No branches: of what is compared in a loop each would cost more than the rest.)
+constexpr int kTokenBits = 20;
 struct Candidate {
     double score;
-    uint32_t beam, token;
-    __device__ bool before(const Candidate &o) const {
-        return score != o.score ? score > o.score : beam != o.beam ? beam < o.beam : token < o.token;
-    }
+    uint32_t id;
+    __device__ bool before(const Candidate &o) const { return (score > o.score) | ((score == o.score) & (id < o.id)); }
 };
 
 __global__ __launch_bounds__(kJoinThreads) void select_join_kernel(SelectArgs a, int group0, int chunks) {
@@ -201,60 +221,80 @@ __global__ __launch_bounds__(kJoinThreads) void select_join_kernel(SelectArgs a,
     const int g = blockIdx.x, keep = a.keep, w = a.beams;
     const int64_t out = (static_cast<int64_t>(group0) + g) * keep;
     if (tid == 0) s_count = 0;
+    // The first candidates are asked for before anything else, all at once, and stay in registers.
+    // They go by their places in the chunks' lists, the first of every list before the second
+    // of any: the lanes of the first waves then hold firsts alone, and the threshold is near.
+    const int lists = w * chunks, all = lists * keep;
+    auto at = [&](int i) {
+        const uint64_t *best = a.best + static_cast<int64_t>(g) * all;
+        const int place = i / lists;
+        return best[(i - place * lists) * keep + place];
+    };
+    uint64_t held[kHeld];
+#pragma unroll
+    for (int r = 0; r < kHeld; ++r) held[r] = tid + r * kJoinThreads < all ? at(tid + r * kJoinThreads) : 0ull;
     // What a row's logits get: its beam's score less the logarithm of its sum.
     bool bad = false;
     for (int b = wave; b < w; b += kJoinThreads / 64) {
         const float2 *sums = a.sums + (static_cast<int64_t>(g) * w + b) * chunks;
-        float m = -__builtin_inff();
-        for (int i = lane; i < chunks; i += 64) m = fmaxf(m, sums[i].x);
+        const float2 mine = lane < chunks ? sums[lane] : float2{-__builtin_inff(), 0.0f};
+        const float score = a.scores[(static_cast<int64_t>(group0) + g) * w + b];
+        float m = mine.x;
+        for (int i = lane + 64; i < chunks; i += 64) m = fmaxf(m, sums[i].x);
 #pragma unroll
         for (int o = 32; o; o >>= 1) m = fmaxf(m, __shfl_xor(m, o, 64));
-        double l = 0.0;
-        for (int i = lane; i < chunks; i += 64)
-            if (sums[i].x > -__builtin_inff()) l += static_cast<double>(sums[i].y) * __builtin_amdgcn_exp2f((sums[i].x - m) * kLog2e);
+        auto part = [&](const float2 &v) { return v.x > -__builtin_inff() ? static_cast<double>(v.y) * __builtin_amdgcn_exp2f((v.x - m) * kLog2e) : 0.0; };
+        double l = part(mine);
+        for (int i = lane + 64; i < chunks; i += 64) l += part(sums[i]);
 #pragma unroll
         for (int o = 32; o; o >>= 1) l += __shfl_xor(l, o, 64);
-        const float score = a.scores[(static_cast<int64_t>(group0) + g) * w + b];
         const bool live = __builtin_isfinite(score), some = __builtin_isfinite(m);
         if (lane == 0) s_add[b] = live && some ? static_cast<double>(score) - m - log(l) : -__builtin_inf();
         bad = bad || (live && !some);
     }
     dev::flag_if(bad && lane == 0, a.err, kErrNoMass);
     __syncthreads();
-    const int per = chunks * keep, all = w * per;
-    const uint64_t *best = a.best + static_cast<int64_t>(g) * all;
-    auto candidate = [&](int i, Candidate &c) {
-        const uint64_t k = best[i];
-        c.beam = static_cast<uint32_t>(i / per);
-        c.token = 0xFFFFFFFFu - static_cast<uint32_t>(k);
-        c.score = s_add[c.beam] + value_of(static_cast<uint32_t>(k >> 32));
+    auto read = [&](int i, uint64_t k, Candidate &c) {
+        const uint32_t beam = static_cast<uint32_t>(i % lists / chunks);
+        c.id = beam << kTokenBits | (0xFFFFFFFFu - static_cast<uint32_t>(k));
+        c.score = s_add[beam] + value_of(static_cast<uint32_t>(k >> 32));
         return k != 0 && c.score > -__builtin_inf();
+    };
+    auto each = [&](auto f) {
+#pragma unroll
+        for (int r = 0; r < kHeld; ++r) {
+            Candidate c;
+            const int i = tid + r * kJoinThreads;
+            if (i < all && read(i, held[r], c)) f(c);
+        }
+        for (int i = tid + kHeld * kJoinThreads; i < all; i += kJoinThreads) {
+            Candidate c;
+            if (read(i, at(i), c)) f(c);
+        }
     };
     // The threshold as in a chunk, on the scores rounded to 32 bits: rounding keeps
     // the order, so that what is below it is behind the candidates that reach it.  (A
     // score below the range of 32 bits has the smallest key that a candidate has.)
-    auto key = [&](const Candidate &c) { return max(key_of(static_cast<float>(c.score)), 1u); };
+    auto key = [&](const Candidate &c) { return max(key_of(static_cast<float>(c.score)), kLeastKey); };
     uint32_t mine = 0;
-    Candidate c;
-    for (int i = tid; i < all; i += kJoinThreads)
-        if (candidate(i, c)) mine = max(mine, key(c));
+    each([&](const Candidate &c) { mine = max(mine, key(c)); });
     const uint32_t reach = reached(mine, keep);
     if (lane == 0) s_reach[wave] = reach;
     __syncthreads();
-    uint32_t limit = 1;
+    uint32_t limit = kLeastKey;
 #pragma unroll
     for (int v = 0; v < kJoinThreads / 64; ++v) limit = max(limit, s_reach[v]);
     if (mine >= limit)
-        for (int i = tid; i < all; i += kJoinThreads)
-            if (candidate(i, c) && key(c) >= limit) {
-                const int at = atomicAdd(&s_count, 1);
-                if (at < kJoinCandidates) s_cand[at] = c;
-            }
+        each([&](const Candidate &c) {
+            if (key(c) < limit) return;
+            const int at = atomicAdd(&s_count, 1);
+            if (at < kJoinCandidates) s_cand[at] = c;
+        });
     __syncthreads();
     auto put = [&](int r, const Candidate &c) {
         a.out_scores[out + r] = static_cast<float>(c.score);
-        a.parents[out + r] = static_cast<int32_t>(c.beam);
-        a.tokens[out + r] = static_cast<int32_t>(c.token);
+        a.parents[out + r] = static_cast<int32_t>(c.id >> kTokenBits);
+        a.tokens[out + r] = static_cast<int32_t>(c.id & ((1u << kTokenBits) - 1));
     };
     auto put_none = [&](int r) {
         a.out_scores[out + r] = -__builtin_inff();
@@ -270,6 +310,7 @@ __global__ __launch_bounds__(kJoinThreads) void select_join_kernel(SelectArgs a,
             }
             const Candidate mine = s_cand[i];
             int rank = 0;
+#pragma unroll 4
             for (int j = 0; j < n; ++j) rank += s_cand[j].before(mine);
             if (rank < keep) put(rank, mine);
         }
@@ -279,13 +320,13 @@ __global__ __launch_bounds__(kJoinThreads) void select_join_kernel(SelectArgs a,
     __shared__ Candidate s_top[kJoinThreads / 64];
     __shared__ Candidate s_last;
     for (int r = 0; r < keep; ++r) {
-        Candidate k{-__builtin_inf(), 0xFFFFFFFFu, 0xFFFFFFFFu};
-        for (int i = tid; i < all; i += kJoinThreads)
-            if (candidate(i, c) && (r == 0 || s_last.before(c)) && c.before(k)) k = c;
+        Candidate k{-__builtin_inf(), 0xFFFFFFFFu};
+        each([&](const Candidate &c) {
+            if ((r == 0 || s_last.before(c)) && c.before(k)) k = c;
+        });
 #pragma unroll
         for (int o = 32; o; o >>= 1) {
-            const Candidate other{__shfl_xor(k.score, o, 64), static_cast<uint32_t>(__shfl_xor(static_cast<int>(k.beam), o, 64)),
-                                  static_cast<uint32_t>(__shfl_xor(static_cast<int>(k.token), o, 64))};
+            const Candidate other{__shfl_xor(k.score, o, 64), static_cast<uint32_t>(__shfl_xor(static_cast<int>(k.id), o, 64))};
             if (other.before(k)) k = other;
         }
         if (lane == 0) s_top[wave] = k;
