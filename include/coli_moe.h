@@ -588,9 +588,10 @@ coli_status coli_latent_read(coli_serve *serve, int32_t cache_kind, const void *
  * table).  The decode calls that follow give what they give after coli_latent_plan, up to
  * the rounding of their sums, and attend to a group's prefix once for all its
  * tokens: to those of its positions that every token of the group sees as context, in
- * whole tiles of 64.  Where the pieces of all sequences and groups would exceed the
- * handle's room (more than four per CU) nothing is shared.  Groups that do not
- * ascend set bit 0 and nothing is shared. */
+ * whole tiles of 64.  Nothing is shared where the pieces of all sequences and groups
+ * would exceed the handle's room (more than four per CU), and in steps of more than 1024
+ * sequences and groups or 65536 tokens.  Groups that do not ascend set bit 0 and
+ * nothing is shared. */
 coli_status coli_latent_plan_shared(coli_serve *serve, const int32_t *q_start, const int32_t *kv_len, int32_t n_seq, int32_t n_tok,
                                     const int32_t *group_start, const int32_t *prefix_len, int32_t n_groups, void *stream);
 
@@ -604,8 +605,8 @@ coli_status coli_latent_plan_shared(coli_serve *serve, const int32_t *q_start, c
  * -inf); where a group has fewer than keep, the rest is -inf, -1 and -1.  A row of a
  * live beam with an infinite logit, or with none above -inf, has no continuation and sets
  * bit 3.  Scores are compared in 64 bits, with the logarithm from a sum of fp32
- * exponentials.  beams and keep up to 64, vocab up to 2^20 (COLI_E_UNSUPPORTED beyond),
- * n_groups * beams up to max_seqs.  The call uses the partial results' room. */
+ * exponentials.  beams and keep up to 64, n_groups * beams up to max_seqs; vocab
+ * beyond 2^20: COLI_E_UNSUPPORTED.  The call uses the partial results' room. */
 coli_status coli_beam_select(coli_serve *serve, const void *logits, int64_t logits_stride, int32_t kind, int32_t vocab,
                              const float *scores, int32_t n_groups, int32_t beams, int32_t keep, float *out_scores,
                              int32_t *out_parents, int32_t *out_tokens, void *stream);

@@ -275,6 +275,16 @@ __global__ __launch_bounds__(kReadThreads) void read_kernel(ReadArgs a) {
         if (tid < kReadRows) s_row[tid] = from;
         dev::flag_if(bad, a.err, kErrSeq);
         dev::flag_if(bad_page, a.err, kErrPage);
+    } else {
+        // Meanwhile the other waves look for bounds that do not ascend: the search passes by
+        // those of sequences that no row of its workgroup falls in.
+        constexpr int kOthers = kReadThreads - 64;
+        bool bad = false;
+        for (int64_t b = static_cast<int64_t>(blockIdx.x) * kOthers + tid - 64; b < a.n_seq; b += static_cast<int64_t>(gridDim.x) * kOthers) {
+            const int k0 = a.k_start[b], k1 = a.k_start[b + 1];
+            bad = bad || k0 < 0 || k1 < k0 || k1 > a.n_rows;
+        }
+        dev::flag_if(bad, a.err, kErrSeq);
     }
     __syncthreads();
     auto load = [](auto *p) {
