@@ -8,7 +8,13 @@
 // in registers.  A second launch, a workgroup to a group, joins the sums of
 // each row and the lists of all rows, the scores taken in 64 bits: the candidates
 // of two beams can lie nearer to each other than the 32-bit roundings of their
-// scores.  Bound by reading the logits.
+// scores.  (One launch, the join by each group's last workgroup: 32 groups of 8 beams of
+// 151643 logits 77 us, as lists are then handed over past the caches, so 42; one group of
+// 4 beams 9.7 and 10.2 us.)
+//
+// Measured, fp32 logits, keep 16: 32 x 8 x 151643, 155 MB, 36 us and 7 for the join (kernel
+// times; both 42 us called in turn): bound by reading the logits, 4.3 TB/s of 5.0 of a large
+// copy.  1 x 4 x 32000, keep 8: 5 and 4.6 us, two launches and their latencies.
 //
 // The best of a chunk: a lane's largest value is known from the pass.  The keep-th
 // largest of a wave's 64 lane maxima is a value that keep elements of the wave
@@ -34,8 +40,10 @@ constexpr uint32_t kLeastKey = 0x00800000u;
 // candidate; -0 and +0 share a key.
 __device__ __forceinline__ uint32_t key_of(float v) { return v > -__builtin_inff() ? dev::float_key(v) : 0u; }
 __device__ __forceinline__ float value_of(uint32_t key) { return __uint_as_float(key & 0x80000000u ? key ^ 0x80000000u : ~key); }
-// A value's key above its token's, lower tokens first.
-__device__ __forceinline__ uint64_t packed(uint32_t key, uint32_t token) { return static_cast<uint64_t>(key) << 32 | (0xFFFFFFFFu - token); }
+// A value's key above its beam and token, lower ones first: the lower bits are their
+// number's complement.
+constexpr int kTokenBits = 20;
+__device__ __forceinline__ uint64_t packed(uint32_t key, uint32_t id) { return static_cast<uint64_t>(key) << 32 | static_cast<uint32_t>(~id); }
 
 // The largest key that `keep` lanes of the wave reach (0 where fewer than that have a
 // candidate), by its bits from the highest down.  (A key that up to a quarter more lanes
@@ -129,7 +137,8 @@ __global__ __launch_bounds__(kThreads) void select_kernel(SelectArgs a, int row0
     uint32_t limit = kLeastKey;
 #pragma unroll
     for (int w = 0; w < kWaves; ++w) limit = max(limit, s_reach[w]);
-    auto token_of = [&](int e) { return static_cast<uint32_t>(first + ((e >> 2) * kThreads + tid) * 4 + (e & 3)); };
+    const int group = row / a.beams, beam = row - group * a.beams;
+    auto id_of = [&](int e) { return static_cast<uint32_t>(beam << kTokenBits | (first + ((e >> 2) * kThreads + tid) * 4 + (e & 3))); };
     const float least = value_of(limit);
     // The threshold is reached by few: a wave looks at one element of all lanes at a time,
     // first to count them, so that it takes its places of the list at once.
@@ -145,7 +154,7 @@ __global__ __launch_bounds__(kThreads) void select_kernel(SelectArgs a, int row0
             const uint64_t m = __ballot(x[e] >= least);
             if (m) {
                 const int at = to + __popcll(m & ((1ull << lane) - 1));
-                if (x[e] >= least && at < kCandidates) s_cand[at] = packed(key_of(x[e]), token_of(e));
+                if (x[e] >= least && at < kCandidates) s_cand[at] = packed(key_of(x[e]), id_of(e));
                 to += __popcll(m);
             }
         }
@@ -162,19 +171,21 @@ __global__ __launch_bounds__(kThreads) void select_kernel(SelectArgs a, int row0
             if (s_max[w] > -__builtin_inff()) l += s_sum[w] * __builtin_amdgcn_exp2f((s_max[w] - m) * kLog2e);
         a.sums[part] = float2{m, l};
     }
-    uint64_t *best = a.best + part * keep;
+    // A group's lists lie place by place: the firsts of all lists, the seconds, ...
+    const int lists = a.beams * chunks;
+    uint64_t *best = a.best + static_cast<int64_t>(group) * lists * keep + beam * chunks + chunk;
     const int n = s_count;
     if (n <= kCandidates) {
         for (int i = tid; i < max(n, keep); i += kThreads) {
             if (i >= n) {
-                best[i] = 0;
+                best[i * lists] = 0;
                 continue;
             }
             const uint64_t k = s_cand[i];
             int rank = 0;
 #pragma unroll 8
             for (int j = 0; j < n; ++j) rank += s_cand[j] > k;
-            if (rank < keep) best[rank] = k;
+            if (rank < keep) best[rank * lists] = k;
         }
         return;
     }
@@ -185,7 +196,7 @@ __global__ __launch_bounds__(kThreads) void select_kernel(SelectArgs a, int row0
 #pragma unroll
         for (int e = 0; e < EACH; ++e) {
             const uint32_t key = key_of(x[e]);
-            const uint64_t v = key ? packed(key, token_of(e)) : 0ull;
+            const uint64_t v = key ? packed(key, id_of(e)) : 0ull;
             if (v < before && v > k) k = v;
         }
 #pragma unroll
@@ -198,14 +209,13 @@ __global__ __launch_bounds__(kThreads) void select_kernel(SelectArgs a, int row0
         __syncthreads();
 #pragma unroll
         for (int w = 0; w < kWaves; ++w) k = s_top[w] > k ? s_top[w] : k;
-        if (tid == 0) best[r] = k;
+        if (tid == 0) best[r * lists] = k;
         before = k;                                       // 0 once there is none left: v < 0 holds for nothing
     }
 }
 
 // A candidate's place: by score, then by beam and token, which `id` holds one above the
 // other.  (No branches: of what is compared in a loop each would cost more than the rest.)
-constexpr int kTokenBits = 20;
 struct Candidate {
     double score;
     uint32_t id;
@@ -222,17 +232,13 @@ __global__ __launch_bounds__(kJoinThreads) void select_join_kernel(SelectArgs a,
     const int64_t out = (static_cast<int64_t>(group0) + g) * keep;
     if (tid == 0) s_count = 0;
     // The first candidates are asked for before anything else, all at once, and stay in registers.
-    // They go by their places in the chunks' lists, the first of every list before the second
+    // They lie by their places in the chunks' lists, the first of every list before the second
     // of any: the lanes of the first waves then hold firsts alone, and the threshold is near.
-    const int lists = w * chunks, all = lists * keep;
-    auto at = [&](int i) {
-        const uint64_t *best = a.best + static_cast<int64_t>(g) * all;
-        const int place = i / lists;
-        return best[(i - place * lists) * keep + place];
-    };
+    const int all = w * chunks * keep;
+    const uint64_t *best = a.best + static_cast<int64_t>(g) * all;
     uint64_t held[kHeld];
 #pragma unroll
-    for (int r = 0; r < kHeld; ++r) held[r] = tid + r * kJoinThreads < all ? at(tid + r * kJoinThreads) : 0ull;
+    for (int r = 0; r < kHeld; ++r) held[r] = tid + r * kJoinThreads < all ? best[tid + r * kJoinThreads] : 0ull;
     // What a row's logits get: its beam's score less the logarithm of its sum.
     bool bad = false;
     for (int b = wave; b < w; b += kJoinThreads / 64) {
@@ -254,22 +260,21 @@ __global__ __launch_bounds__(kJoinThreads) void select_join_kernel(SelectArgs a,
     }
     dev::flag_if(bad && lane == 0, a.err, kErrNoMass);
     __syncthreads();
-    auto read = [&](int i, uint64_t k, Candidate &c) {
-        const uint32_t beam = static_cast<uint32_t>(i % lists / chunks);
-        c.id = beam << kTokenBits | (0xFFFFFFFFu - static_cast<uint32_t>(k));
-        c.score = s_add[beam] + value_of(static_cast<uint32_t>(k >> 32));
-        return k != 0 && c.score > -__builtin_inf();
+    auto read = [&](uint64_t k, Candidate &c) {
+        if (k == 0) return false;
+        c.id = ~static_cast<uint32_t>(k);
+        c.score = s_add[c.id >> kTokenBits] + value_of(static_cast<uint32_t>(k >> 32));
+        return c.score > -__builtin_inf();
     };
     auto each = [&](auto f) {
 #pragma unroll
         for (int r = 0; r < kHeld; ++r) {
             Candidate c;
-            const int i = tid + r * kJoinThreads;
-            if (i < all && read(i, held[r], c)) f(c);
+            if (read(held[r], c)) f(c);
         }
         for (int i = tid + kHeld * kJoinThreads; i < all; i += kJoinThreads) {
             Candidate c;
-            if (read(i, at(i), c)) f(c);
+            if (read(best[i], c)) f(c);
         }
     };
     // The threshold as in a chunk, on the scores rounded to 32 bits: rounding keeps

@@ -364,9 +364,8 @@ class Serve:
         ps = self._dense("scores", scores, torch.float32, (groups, beams))
         if keep < 1:
             raise ValueError(f"keep {keep} must be >= 1")
-        best = torch.empty(groups, keep, dtype=torch.float32, device=self.device)
-        both = torch.empty(2, groups, keep, dtype=torch.int32, device=self.device)
-        parents, tokens = both[0], both[1]
+        best, parents, tokens = torch.empty(3, groups, keep, dtype=torch.int32, device=self.device).unbind()
+        best = best.view(torch.float32)
         self._call(_select, pl, logits.stride()[0] if n > 1 else vocab, kind, vocab, ps, groups, beams, keep, best.data_ptr(), parents.data_ptr(), tokens.data_ptr())
         return best, parents, tokens
 
