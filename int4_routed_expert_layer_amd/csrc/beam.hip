@@ -357,9 +357,11 @@ void launch_chunks(const SelectArgs &a, int row0, int rows, int chunks, hipStrea
 }  // namespace
 
 hipError_t launch_select(const SelectArgs &a, int n_cu, hipStream_t s) {
-    // Chunks of 8192 elements, or of 2048 where those would leave CUs idle.
+    // Chunks of 8192 elements; of 2048 where those are few: replayed from a graph, 4 rows of
+    // 32000 take 9.1 us in small and 10.6 in large ones, one of 151643 9.3 and 10.5, 4 of 151643
+    // (76 large chunks) 11.1 and 11.0, 16 13.4 and 12.4, 256 69.6 and 42.4.  (4096 there: 49.)
     const int64_t rows = static_cast<int64_t>(a.n_groups) * a.beams;
-    const bool small = rows * ((a.vocab + 8191) / 8192) < 2 * n_cu;
+    const bool small = rows * ((a.vocab + 8191) / 8192) < n_cu / 4;
     const int each = small ? 2048 : 8192, chunks = (a.vocab + each - 1) / each;
     // As many groups in a launch as the scratch holds.
     const int64_t per = static_cast<int64_t>(a.beams) * chunks;
