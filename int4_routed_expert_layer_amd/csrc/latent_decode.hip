@@ -870,6 +870,7 @@ constexpr float kTileTime = 1.4f, kPieceTime = 0.06f;   // of 16 pieces' joining
 constexpr int kSortMost = 1024; // sequences that are put in order
 static_assert(kPrefixEntries == kSortMost && kPrefixEntries == kPlanThreads, "an entry to a thread, all of them in LDS");
 constexpr int kItemLanes = 16;  // lanes that write a sequence's items
+constexpr int kLengthBits = 7, kLengths = 1 << kLengthBits;
 
 __device__ __forceinline__ int cut(int tiles, int per) { return max(1, (tiles + per - 1) / per); }
 
@@ -1044,6 +1045,7 @@ __global__ __launch_bounds__(kPlanThreads) void decode_plan_kernel(DecodePlan p,
     };
     int best = 0;
     long long best_cost = 0;
+    int run1 = most, run2 = 0;                           // the smallest runs that fit one round and two
     for (int r = 1; r <= 4; ++r) {
         const unsigned long long room = static_cast<unsigned long long>(r) * n_cu;
         if (units > room) continue;
@@ -1066,6 +1068,8 @@ __global__ __launch_bounds__(kPlanThreads) void decode_plan_kernel(DecodePlan p,
             lo = w == 0 ? lo : min(lo + step * (w - 1) + 1, top);
             hi = top;
         }
+        if (r == 1) run1 = hi;
+        if (r == 2) run2 = hi;
         if (r == 1) {
             // The smallest that fits, or one up to 4.75 times as long whose fewer
             // pieces are joined the sooner.
@@ -1088,6 +1092,55 @@ __global__ __launch_bounds__(kPlanThreads) void decode_plan_kernel(DecodePlan p,
         if (best == 0 || cost < best_cost) {
             best = hi;
             best_cost = cost;
+        }
+    }
+    if constexpr (PREFIX) {
+        // Prefixes give long runs beside the short ones of the sequences: between one round and
+        // two lie runs of which the long ones have a CU each and the short ones share the
+        // others.  Sixteen of them, a wave each, laid out on a histogram of the lengths.
+        // (64 sequences of 20 to 2000 tokens behind 32000, 16 heads: the fullest CU 39
+        // tiles, so 43 at a mean of 36, and 288 pieces, so 503.)
+        if (run2 > 0 && run2 + 1 < run1) {
+            __shared__ int s_hist[kPlanThreads / 64][kLengths];
+            const int mine = run2 + 1 + static_cast<int>(static_cast<int64_t>(run1 - run2 - 1) * wave / (kPlanThreads / 64));
+            const int scale = max(0, 32 - __clz(run1) - kLengthBits);
+            int *hist = s_hist[wave];
+            for (int i = lane; i < kLengths; i += 64) hist[i] = 0;
+            __syncthreads();
+            for (int b = lane; b < n_seq; b += 64) {
+                const int4 v = s_seq[b];
+                if (v.x == 0) continue;
+                const int split = cut(v.y, mine), each = v.y / split, over = v.y - each * split;
+                atomicAdd(hist + (each >> scale), v.x * (split - over));
+                if (over) atomicAdd(hist + ((each + 1) >> scale), v.x * over);
+            }
+            __syncthreads();
+            // How many are as long as each length: two of them a lane, from the longest down.
+            static_assert(kLengths == 128, "two lengths a lane");
+            const int at = kLengths - 1 - 2 * lane, longer = hist[at], here = longer + hist[at - 1], sum = dev::running_sum(here);
+            hist[at] = sum - here + longer;
+            hist[at - 1] = sum;
+            __syncthreads();
+            const int n = __builtin_amdgcn_readlane(sum, 63);
+            auto load_of = [&](int i) {                  // of the i-th longest run
+                if (i >= n) return 0.0f;
+                int x = 0;
+                for (int step = kLengths / 2; step; step >>= 1)
+                    if (hist[x + step] > i) x += step;
+                return static_cast<float>(((x + 1) << scale) - 1 + kItemCost);
+            };
+            float fullest = 0.0f;
+            for (int k = lane; k < n_cu; k += 64) fullest = fmaxf(fullest, load_of(k) + load_of(2 * n_cu - 1 - k));
+#pragma unroll
+            for (int o = 32; o; o >>= 1) fullest = fmaxf(fullest, __shfl_xor(fullest, o, 64));
+            if (lane == 0) s_cost[wave] = fullest * kJoinItems + static_cast<float>(n);
+            __syncthreads();
+            const float mycost = s_cost[lane & 15];
+            float least = mycost;
+#pragma unroll
+            for (int o = 8; o; o >>= 1) least = fminf(least, __shfl_xor(least, o, 64));
+            const int w = __ffsll(__ballot(mycost == least)) - 1;
+            if (best == 0 || least < static_cast<float>(best_cost)) best = run2 + 1 + static_cast<int>(static_cast<int64_t>(run1 - run2 - 1) * w / (kPlanThreads / 64));
         }
     }
     if (best == 0) best = static_cast<int>((s_work + n_cu - 1) / n_cu);
