@@ -36,6 +36,13 @@
 // product; the matrix pipes are busy 43% of the cycles at 2.1 GHz, the product's 70%
 // at 1.5 to 1.9.  One token, 4k, 64 heads: 11.5 and 5.7 us, a chain of latencies (the
 // item, its queries, page numbers, keys, four steps, partial results).
+//
+// Over an 8-bit cache the summing waves also convert (Source8).  64 tokens of
+// sequences up to 12k, 64 heads, f16: 69 us and 9.4 for the join, 204 MB; one token, 4k:
+// 12.7 and 5.2.  Bound by its steps, 1.3 us each: 64 tokens of 8192 take 110 us, 111 from
+// 16 bits; 84 without the copies, and resident 100, 81 without the conversion.
+// A unit of 32 rows or fewer does half of the products (16 heads, 64 tokens of 8192: 8
+// bits 109 -> 94 us, 16 bits 112 -> 108).
 #include "dev_attn.h"
 
 namespace coli {
@@ -131,6 +138,10 @@ __device__ __forceinline__ void clean(const Shared &sh, int t) {
 // the ring as the 16-bit values that they stand for: the scoring waves work as on a
 // 16-bit cache.  (Every stored value is one of the 16-bit type: the scales are powers of
 // two within its range.)  A wave waits for its own copies alone.
+// 64 tokens of 8192, 64 heads: 110 us.  With the bytes in registers instead of LDS until
+// their step 67 spill; with all eight waves converting four keys 112 to 116, with scoring
+// waves converting what they score 114, with values read a step ahead and three steps on
+// their way 110 to 114.
 template <bool ONCE>
 struct Source8 {
     static constexpr int kUnits = kRow8Bytes / 16, kKeys = 8, kCopies = (kKeys * kUnits + 63) / 64;
@@ -879,7 +890,12 @@ __device__ __forceinline__ int cut(int tiles, int per) { return max(1, (tiles + 
 // tokens, which are neighbours, are its rows, and its keys are the prefix's whole
 // tiles, found through the first sequence's row of the block table.  No more than what
 // every token of the group sees as context is shared, so that nothing of it is
-// masked; the sequences begin behind it.  Both leave pieces for the join.
+// masked; the sequences begin behind it.  Both leave pieces for the join, which goes by
+// the group's 64-row units and finds each row's own pieces by its token's record: by the
+// sequences' units, of 16 rows each, it read the prefix's pieces four times over (64
+// sequences behind 32000 tokens, 16 heads: 23 us, so 11).  That step: 89 us, 72 GF, of
+// 80 MB where the 64 contexts are 2.4 GB; its plan 29 us, that of eight sequences behind
+// 4096 tokens 15.
 struct Groups {
     const int32_t *start, *prefix;     // [n + 1] first sequences; [n] tokens
     int n;
