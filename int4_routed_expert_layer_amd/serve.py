@@ -136,6 +136,13 @@ class Serve:
 
     def _cache(self, cache, layers=()):
         """Address, page stride, pages and whether it is of 8 bits; `layers` is () or the leading (n_layers,)."""
+        try:
+            kind, shape, strides = cache.dtype, cache.shape, cache.stride()
+            width = ROW8 if kind is torch.uint8 else ROW if kind is self.dtype else 0
+            if len(shape) == 3 + len(layers) and shape[-1] == width == strides[-2] and shape[-2] == self.page_size and strides[-1] == 1 and shape[-3] > 1 and cache.get_device() == self.index:
+                return cache.data_ptr(), strides[-3], shape[-3], width == ROW8
+        except (AttributeError, IndexError):
+            pass
         pages = self._sizes("cache", cache, 3 + len(layers))[-3]
         eight = cache.dtype is torch.uint8
         width = ROW8 if eight else ROW
@@ -153,6 +160,13 @@ class Serve:
         return *self._cache(cache), 1, 0
 
     def _table(self, block_table, n_seq):
+        try:
+            rows, cols = block_table.shape
+            row, step = block_table.stride()
+            if rows == n_seq and step == 1 and block_table.dtype is torch.int32 and block_table.get_device() == self.index:
+                return block_table.data_ptr(), row, cols
+        except (AttributeError, ValueError):
+            pass
         cols = self._sizes("block_table", block_table, 2)[1]
         return self._rows("block_table", block_table, torch.int32, (n_seq, cols)), block_table.stride()[0], cols
 
