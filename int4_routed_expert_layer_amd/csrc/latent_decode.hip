@@ -42,7 +42,8 @@
 // 12.7 and 5.2.  Bound by its steps, 1.3 us each: 64 tokens of 8192 take 110 us, 111 from
 // 16 bits; 84 without the copies, and resident 100, 81 without the conversion.
 // A unit of 32 rows or fewer does half of the products (16 heads, 64 tokens of 8192: 8
-// bits 109 -> 94 us, 16 bits 112 -> 108).
+// bits 109 -> 94 us, 16 bits 112 -> 108) and leaves half a piece (16 heads, 32 tokens of
+// 600 to 12000: 48.9 -> 45.5).
 #include "dev_attn.h"
 
 namespace coli {
@@ -746,16 +747,19 @@ __global__ __launch_bounds__(kThreads, 2) void latent_decode_kernel(DecodeArgs a
                 }
             } else {
                 // Sixteen bytes per lane, a wave's 1 KB together (rows would
-                // spread each store over 32 of them).
+                // spread each store over 32 of them).  Of 32 rows or fewer the other half is
+                // neither written nor read.
                 f32x4 *part = reinterpret_cast<f32x4 *>(a.part + static_cast<int64_t>(it.slot) * kTileRows * kLatent) + w * 32 * 64 + lane;
 #pragma unroll
                 for (int cb = 0; cb < 4; ++cb)
 #pragma unroll
-                    for (int rb = 0; rb < 2; ++rb)
+                    for (int rb = 0; rb < 2; ++rb) {
+                        if (rb == 1 && rows <= 32) continue;
 #pragma unroll
                         for (int g = 0; g < 4; ++g)
                             part[((cb * 2 + rb) * 4 + g) * 64] = f32x4{acc[cb][rb][4 * g], acc[cb][rb][4 * g + 1],
                                                                        acc[cb][rb][4 * g + 2], acc[cb][rb][4 * g + 3]};
+                    }
             }
         }
     }
@@ -786,6 +790,7 @@ __global__ __launch_bounds__(256) void join_kernel(DecodeArgs a) {
         const bool group = u.split & kJoinGroup;
         u.split &= ~kJoinGroup;
         const int block = apart ? 4 * (wg % per) + wave : wg % per;
+        if (32 * (block & 1) >= u.rows) continue;         // (a workgroup's, where its waves meet)
         const int r = 32 * (block & 1) + (lane & 31);
         const bool live = r < u.rows;                     // partial rows past the unit's hold no statistics
         const float *ml = a.part_ml + (static_cast<int64_t>(u.slot0) * kTileRows + (live ? r : 0)) * 2;
