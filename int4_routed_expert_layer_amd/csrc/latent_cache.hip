@@ -222,17 +222,21 @@ __global__ __launch_bounds__(kKeepThreads) void keep_kernel(KeepArgs a, int64_t 
 }
 
 // Read.  Output row t is position first[b] + t - k_start[b] of the sequence b that it
-// falls in.  A workgroup takes 16 rows: a wave finds their sequences (64 bounds at a time)
-// and addresses, then each thread moves 16-byte units of output, six in flight.  Rows
-// before the first sequence and behind the last are left alone.
-constexpr int kReadRows = 16, kReadThreads = 192;
+// falls in.  A workgroup takes 8 rows: a wave finds their sequences (64 bounds at a time)
+// and addresses, then each thread moves three 16-byte units of output.  Rows of 8 bits come
+// by way of LDS, as they lie, and are converted from there: eight values and their scale
+// loaded by each thread as it needs them, 16 rows a workgroup, took 97 us for what now
+// takes 79.  Rows before the first sequence and behind the last are left alone.
+// Sixteen contexts of 8787 to 32767 rows, 8 bits, 448 MB: 79 us, 5.7 TB/s; 16 of 16384, 16
+// bits, 604 MB: 102 us, 5.9; eight up to 1023 rows 3.8 us, a chain of dependent loads
+// (bound, page, row).  16 rows by 384 threads take the same; by 192 85 and 121, by 576 107 and
+// 100; 8 rows by 288 98 and 104, 4 by 96 85 and 110.
+constexpr int kReadRows = 8, kReadThreads = 192;
 constexpr int kOutUnits = kRowBytes / 16, kReadEach = kReadRows * kOutUnits / kReadThreads;
 static_assert(kReadEach * kReadThreads == kReadRows * kOutUnits, "whole rounds of units");
 
-// Loads are of data read once.  With STREAM the stores bypass the caches too: sixteen contexts
-// of 8787 to 32767 rows, 8 bits, 448 MB, 106 us, with such loads 100, with both 96 (4.7
-// TB/s; HBM); of fewer rows than the caches hold, what comes next finds them there.  Eight
-// contexts up to 1023 rows: 5.2 us, a chain of dependent loads (bound, page, row).
+// With STREAM the stores bypass the caches: 16 contexts of 16384 rows, 16 bits, 113 us, so
+// 102 (8 bits the same).  Of fewer bytes what comes next finds them there.
 constexpr int64_t kStreamBytes = 64 << 20;
 
 template <bool BF, bool Q8, bool STREAM>
@@ -291,23 +295,42 @@ __global__ __launch_bounds__(kReadThreads) void read_kernel(ReadArgs a) {
     __syncthreads();
     auto load = [](auto *p) {
         typedef std::remove_const_t<std::remove_pointer_t<decltype(p)>> T;
-        return __builtin_nontemporal_load((const __attribute__((address_space(1))) T *)(p));
+        return *(const __attribute__((address_space(1))) T *)(p);
     };
     u32x4 v[kReadEach];
     uint32_t by[kReadEach];
+    __shared__ __align__(16) uint8_t s_raw[Q8 ? kReadRows * kRow8Bytes : 16];
+    if constexpr (Q8) {
+        // The rows' bytes as they lie, by way of LDS.
+        constexpr int kUnits = kRow8Bytes / 16, kEach = (kReadRows * kUnits + kReadThreads - 1) / kReadThreads;
+        u32x4 raw[kEach];
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+            const int g = tid + i * kReadThreads, r = min(g / kUnits, kReadRows - 1), u = g - r * kUnits;
+            const uint8_t *from = g < kReadRows * kUnits ? s_row[r] : nullptr;
+            if (from) raw[i] = load(reinterpret_cast<const u32x4 *>(from + 16 * u));
+        }
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+            const int g = tid + i * kReadThreads;
+            if (g < kReadRows * kUnits) *reinterpret_cast<u32x4 *>(s_raw + 16 * g) = raw[i];
+        }
+        __syncthreads();
+    }
 #pragma unroll
     for (int i = 0; i < kReadEach; ++i) {
         const int g = tid + i * kReadThreads, r = g / kOutUnits, u = g - r * kOutUnits;
         const uint8_t *from = s_row[r];
         if (!from) continue;
+        const uint8_t *raw = s_raw + r * kRow8Bytes;
         if constexpr (!Q8) {
             v[i] = load(reinterpret_cast<const u32x4 *>(from + 16 * u));
         } else if (u < kLatent / 8) {
-            const u32x2 q = load(reinterpret_cast<const u32x2 *>(from + 8 * u));
+            const u32x2 q = *reinterpret_cast<const u32x2 *>(raw + 8 * u);
             v[i] = u32x4{q[0], q[1], 0, 0};
-            by[i] = *(const __attribute__((address_space(1))) uint8_t *)(from + kRow8Scales + u / 4);
+            by[i] = raw[kRow8Scales + u / 4];
         } else {
-            v[i] = load(reinterpret_cast<const u32x4 *>(from + kRow8Rope + 16 * (u - kLatent / 8)));
+            v[i] = *reinterpret_cast<const u32x4 *>(raw + kRow8Rope + 16 * (u - kLatent / 8));
         }
     }
 #pragma unroll
