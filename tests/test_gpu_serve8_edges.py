@@ -1,6 +1,6 @@
 """Calls of the 8-bit cache's, prefix and beam operators at the edges of what they allow: bounds that do not ascend
-where no row falls, other numbers of sequences than a workgroup looks at, and a step planned beside calls that use the
-same scratch."""
+where no row falls, other numbers of sequences than a workgroup looks at, a step planned beside calls that use the
+same scratch, and long prefixes beside short sequences."""
 import numpy as np
 import pytest
 
@@ -15,6 +15,7 @@ if not torch.cuda.is_available():
 from int4_routed_expert_layer_amd.serve import Serve  # noqa: E402
 from test_gpu_latent_cache import DEV  # noqa: E402
 from test_gpu_latent8_cache import Paged, ints  # noqa: E402
+from test_gpu_prefix_decode import Shared  # noqa: E402
 
 
 @pytest.mark.parametrize("bits", [8, 16])
@@ -53,3 +54,12 @@ def test_selection_between_a_plan_and_its_decode():
         assert all(torch.equal(a, b) for a, b in zip(s.beam_select(logits, scores, 4), best))
     assert s.device_errors() == 0
     s.close()
+
+
+@pytest.mark.parametrize("bits", [16, 8])
+@pytest.mark.parametrize("prefix,n,heads,own", [(9000, 40, 16, 700), (700, 260, 16, 130), (16500, 20, 64, 200)])
+def test_long_prefixes_beside_short_sequences_of_few_rows(prefix, n, heads, own, bits):
+    """Plans of more items than CUs whose long runs have a CU to themselves, and pieces of 32 rows or fewer."""
+    r = np.random.default_rng(n)
+    c = Shared([(prefix, [int(x) for x in r.integers(1, own, n)], [1] * n)], heads, 64, "f16", bits, seed=n)
+    c.check(*c.run(), heads=[0, heads - 1])
