@@ -114,9 +114,11 @@ __global__ __launch_bounds__(kThreads) void select_kernel(SelectArgs a, int row0
 #pragma unroll
     for (int o = 32; o; o >>= 1) top = fmaxf(top, __shfl_xor(top, o, 64));
     float sum = 0.0f;
-    if (fabsf(top) < 0x1p100f) {
+    if (fabsf(top) < 0x1p16f) {
         // 2^(z log2 e - top log2 e) by one multiply-add, rounded where it is small; the
-        // rounding of the product with top, the same for all, is taken back behind the sum.
+        // rounding of the product with top, the same for all, is taken back behind the sum:
+        // 2^-8 at most here, and a power of two near 1.  (It grows with top: from 2^31 on that
+        // power can leave the range of fp32.)
         const float c = top * kLog2e, left = __builtin_fmaf(top, kLog2e, -c);
 #pragma unroll
         for (int e = 0; e < EACH; ++e) sum += __builtin_amdgcn_exp2f(__builtin_fmaf(x[e], kLog2e, -c));
