@@ -227,6 +227,7 @@ struct Candidate {
 __global__ __launch_bounds__(kJoinThreads) void select_join_kernel(SelectArgs a, int group0, int chunks) {
     __shared__ Candidate s_cand[kJoinCandidates];
     __shared__ double s_add[kBeamMost];
+    __shared__ float s_most[kBeamMost];
     __shared__ uint32_t s_reach[kJoinThreads / 64];
     __shared__ int s_count;
     const int tid = threadIdx.x, lane = tid & 63, wave = dev::wave_id();
@@ -241,7 +242,9 @@ __global__ __launch_bounds__(kJoinThreads) void select_join_kernel(SelectArgs a,
     uint64_t held[kHeld];
 #pragma unroll
     for (int r = 0; r < kHeld; ++r) held[r] = tid + r * kJoinThreads < all ? best[tid + r * kJoinThreads] : 0ull;
-    // What a row's logits get: its beam's score less the logarithm of its sum.
+    // A row's greatest logit, which its logits are taken from first (in 64 bits a logit of
+    // 1e20 would swallow the rest), and what is added then: its beam's score less the
+    // logarithm of the sum.
     bool bad = false;
     for (int b = wave; b < w; b += kJoinThreads / 64) {
         const float2 *sums = a.sums + (static_cast<int64_t>(g) * w + b) * chunks;
@@ -257,7 +260,10 @@ __global__ __launch_bounds__(kJoinThreads) void select_join_kernel(SelectArgs a,
 #pragma unroll
         for (int o = 32; o; o >>= 1) l += __shfl_xor(l, o, 64);
         const bool live = __builtin_isfinite(score), some = __builtin_isfinite(m);
-        if (lane == 0) s_add[b] = live && some ? static_cast<double>(score) - m - log(l) : -__builtin_inf();
+        if (lane == 0) {
+            s_most[b] = m;
+            s_add[b] = live && some ? static_cast<double>(score) - log(l) : -__builtin_inf();
+        }
         bad = bad || (live && !some);
     }
     dev::flag_if(bad && lane == 0, a.err, kErrNoMass);
@@ -265,7 +271,8 @@ __global__ __launch_bounds__(kJoinThreads) void select_join_kernel(SelectArgs a,
     auto read = [&](uint64_t k, Candidate &c) {
         if (k == 0) return false;
         c.id = ~static_cast<uint32_t>(k);
-        c.score = s_add[c.id >> kTokenBits] + value_of(static_cast<uint32_t>(k >> 32));
+        const int b = c.id >> kTokenBits;
+        c.score = s_add[b] + (static_cast<double>(value_of(static_cast<uint32_t>(k >> 32))) - s_most[b]);
         return c.score > -__builtin_inf();
     };
     auto each = [&](auto f) {

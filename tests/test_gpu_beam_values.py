@@ -1,5 +1,5 @@
 """Beam selection where logits and scores are far from ordinary ones: tokens masked with large negative values of
-their type, and every kind of NaN, in vocabularies of either chunk size."""
+their type, single large logits, rows far from zero, and every kind of NaN, in vocabularies of either chunk size."""
 import numpy as np
 import pytest
 
@@ -68,6 +68,28 @@ def test_tokens_masked_with_a_large_value(g, b, v, value, kind):
     logits, scores = normal(g, b, v, kind, 12)
     logits[:, :, :v - 300] = value
     check(logits, scores, 16)
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("value", [1e9, 6e9, 1e10, 1e20, 1e30, 3e38])
+@pytest.mark.parametrize("g,b,v", SIZES)
+def test_single_large_logits(g, b, v, value, kind):
+    """The token that holds it has all the probability; what follows is as far behind as the logits are apart."""
+    logits, scores = normal(g, b, v, kind, 13)
+    logits[:, 0, 3], logits[:, b - 1, v - 1] = value, value
+    check(logits, scores, 2)
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("value", [-1e10, -1e12, -1e20, -3e38, 1e9, 1e20, 3e38])
+@pytest.mark.parametrize("g,b,v", SIZES)
+def test_rows_that_lie_far_from_zero(g, b, v, value, kind):
+    """Rows of one large value each: every token of a row has the same share of its beam's score, whatever the value."""
+    logits, scores = normal(g, b, v, kind, 16)
+    logits[:, 0], logits[:, b - 1] = value, -value / 4
+    check(logits, scores, 12)
+    scores[:, 0] += 8
+    check(logits, scores, 12)
 
 
 @pytest.mark.parametrize("g,b,v", SIZES)
