@@ -599,8 +599,9 @@ coli_status coli_latent_plan_shared(coli_serve *serve, const int32_t *q_start, c
  * beams x vocab] of `kind`, row stride logits_stride) holds the logits z behind beam b
  * of group g, scores[g * beams + b] (fp32) its score.  The score of token x behind b is
  * score_b + z_x - log sum_y exp z_y.  Outputs [n_groups x keep]: the keep best over all
- * beams and tokens, from the best down, equal ones in the order of beams and then
- * tokens: their scores (fp32), beams and tokens (int32).  A beam whose score is not
+ * beams and tokens, from the best down, equal ones in the order of beams, then of
+ * logits (where 64 bits hold two of a beam as one) and then of tokens: their scores
+ * (fp32), beams and tokens (int32).  A beam whose score is not
  * finite has no continuation, nor has a token whose logit is -inf or NaN (it counts as
  * -inf); where a group has fewer than keep, the rest is -inf, -1 and -1.  A row of a
  * live beam with an infinite logit, or with none above -inf, has no continuation and sets

@@ -216,12 +216,14 @@ __global__ __launch_bounds__(kThreads) void select_kernel(SelectArgs a, int row0
     }
 }
 
-// A candidate's place: by score, then by beam and token, which `id` holds one above the
-// other.  (No branches: of what is compared in a loop each would cost more than the rest.)
+// A candidate's place: by score, then by beam, by logit (two of one beam may have scores
+// that are the same in 64 bits; the greater logit is the first then as in the chunks' lists)
+// and by token.  `rest` holds the three one above the other, the logit as its key's
+// complement.  (No branches: of what is compared in a loop each would cost more than the rest.)
 struct Candidate {
     double score;
-    uint32_t id;
-    __device__ bool before(const Candidate &o) const { return (score > o.score) | ((score == o.score) & (id < o.id)); }
+    uint64_t rest;
+    __device__ bool before(const Candidate &o) const { return (score > o.score) | ((score == o.score) & (rest < o.rest)); }
 };
 
 __global__ __launch_bounds__(kJoinThreads) void select_join_kernel(SelectArgs a, int group0, int chunks) {
@@ -270,9 +272,10 @@ __global__ __launch_bounds__(kJoinThreads) void select_join_kernel(SelectArgs a,
     __syncthreads();
     auto read = [&](uint64_t k, Candidate &c) {
         if (k == 0) return false;
-        c.id = ~static_cast<uint32_t>(k);
-        const int b = c.id >> kTokenBits;
-        c.score = s_add[b] + (static_cast<double>(value_of(static_cast<uint32_t>(k >> 32))) - s_most[b]);
+        const uint32_t id = ~static_cast<uint32_t>(k), key = static_cast<uint32_t>(k >> 32);
+        const int b = id >> kTokenBits;
+        c.rest = static_cast<uint64_t>(b) << (32 + kTokenBits) | static_cast<uint64_t>(~key) << kTokenBits | (id & ((1u << kTokenBits) - 1));
+        c.score = s_add[b] + (static_cast<double>(value_of(key)) - s_most[b]);
         return c.score > -__builtin_inf();
     };
     auto each = [&](auto f) {
@@ -307,8 +310,8 @@ __global__ __launch_bounds__(kJoinThreads) void select_join_kernel(SelectArgs a,
     __syncthreads();
     auto put = [&](int r, const Candidate &c) {
         a.out_scores[out + r] = static_cast<float>(c.score);
-        a.parents[out + r] = static_cast<int32_t>(c.id >> kTokenBits);
-        a.tokens[out + r] = static_cast<int32_t>(c.id & ((1u << kTokenBits) - 1));
+        a.parents[out + r] = static_cast<int32_t>(c.rest >> (32 + kTokenBits));
+        a.tokens[out + r] = static_cast<int32_t>(c.rest & ((1u << kTokenBits) - 1));
     };
     auto put_none = [&](int r) {
         a.out_scores[out + r] = -__builtin_inff();
@@ -334,13 +337,13 @@ __global__ __launch_bounds__(kJoinThreads) void select_join_kernel(SelectArgs a,
     __shared__ Candidate s_top[kJoinThreads / 64];
     __shared__ Candidate s_last;
     for (int r = 0; r < keep; ++r) {
-        Candidate k{-__builtin_inf(), 0xFFFFFFFFu};
+        Candidate k{-__builtin_inf(), ~0ull};
         each([&](const Candidate &c) {
             if ((r == 0 || s_last.before(c)) && c.before(k)) k = c;
         });
 #pragma unroll
         for (int o = 32; o; o >>= 1) {
-            const Candidate other{__shfl_xor(k.score, o, 64), static_cast<uint32_t>(__shfl_xor(static_cast<int>(k.id), o, 64))};
+            const Candidate other{__shfl_xor(k.score, o, 64), __shfl_xor(k.rest, o, 64)};
             if (other.before(k)) k = other;
         }
         if (lane == 0) s_top[wave] = k;

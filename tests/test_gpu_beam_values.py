@@ -111,3 +111,19 @@ def test_every_nan_counts_as_minus_infinity(g, b, v, kind, bits):
         raw[:, :, 2 * i::11] = x
         raw[:, :, 2 * i + 1::11] = x + sign
     check(logits, scores, 9)
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("low", [-1e9, -1e20, -1e30])
+@pytest.mark.parametrize("g,b,v", SIZES)
+def test_scores_that_swallow_the_logits(g, b, v, low, kind):
+    """Beams that begin with a very low score in place of -inf: the 64-bit scores of their tokens coincide, but within a beam
+    the greater logit still comes first; equal scores of different beams go by the beam."""
+    logits, scores = normal(g, b, v, kind, 17)
+    scores[:] = low
+    check(logits, scores, 9)
+    scores[:, 0] = -1
+    logits[:, 0, 4:] = -float("inf")                          # four tokens of the first beam, then those of others
+    check(logits, scores, 12)
+    logits = (1 + torch.arange(v).remainder(89) * 2.0 ** -23).expand(g, b, v).contiguous().to(TYPE[kind])
+    check(logits, scores, 12)                                 # neighbours in fp32
