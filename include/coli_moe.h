@@ -616,8 +616,8 @@ coli_status coli_beam_select(coli_serve *serve, const void *logits, int64_t logi
  * parents[g * beams + j] (0..beams - 1) of it.  The beams of a group have one length,
  * kv_len[g * beams + j], and share pages before their last one at most: the page of
  * position kv_len, if any, and those behind it are each beam's own.  out_table (int32
- * [n_groups * beams x table_cols], not overlapping block_table) gets the places' block
- * tables: p's pages before that of position kv_len, and from there on the own pages of
+ * [n_groups * beams x table_cols], with no element of block_table: apart from it, or row
+ * beside row at one stride) gets the places' block tables: p's pages before that of position kv_len, and from there on the own pages of
  * one old beam each: p's for the first place that continues p, for any other those of a
  * beam that no place continues, in ascending order.  To these the rows of p's last page
  * are copied, in each of n_layers caches (layer_stride apart).  A parent of -1: the

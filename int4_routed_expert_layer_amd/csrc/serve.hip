@@ -141,6 +141,16 @@ coli_status check_counts(coli_serve *S, int32_t n_tok, int32_t n_seq) {
         if (!(cond)) return fail(S, COLI_E_INVALID, __VA_ARGS__);      \
     } while (0)
 
+// Whether two tables of `rows` rows of `cols` share no element: they lie one behind the
+// other, or row beside row at one stride.
+bool tables_apart(const int32_t *a, int64_t a_stride, const int32_t *b, int64_t b_stride, int64_t rows, int64_t cols) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b), width = cols * sizeof(int32_t);
+    if (x + (rows - 1) * a_stride * sizeof(int32_t) + width <= y || y + (rows - 1) * b_stride * sizeof(int32_t) + width <= x) return true;
+    if (rows == 1 || a_stride != b_stride) return false;
+    const uintptr_t stride = a_stride * sizeof(int32_t), far = (y > x ? y - x : x - y) % stride;   // (the same answer whichever lies first)
+    return far >= width && far + width <= stride;
+}
+
 coli_status append_rows(coli_serve *S, bool cache8, const void *c, int64_t c_stride, const void *norm_weight, float eps, const float *cos_table,
                                const float *sin_table, int32_t n_positions, int32_t interleaved, const int32_t *positions,
                                const int64_t *slots, int32_t n_tok, void *cache, int64_t page_stride, int32_t n_pages, const void *q_pe,
@@ -476,9 +486,7 @@ coli_status coli_beam_reorder(coli_serve *S, int32_t cache_kind, void *cache, in
     NEED(block_table && kv_len && parents && out_table, "NULL device pointer");
     const int64_t rows = static_cast<int64_t>(n_groups) * beams;
     NEED(rows == 1 || (table_stride >= table_cols && out_stride >= table_cols), "table strides must be >= table_cols");
-    const uintptr_t x = reinterpret_cast<uintptr_t>(block_table), y = reinterpret_cast<uintptr_t>(out_table);
-    const uintptr_t xs = ((rows - 1) * table_stride + table_cols) * sizeof(int32_t), ys = ((rows - 1) * out_stride + table_cols) * sizeof(int32_t);
-    NEED(x + xs <= y || y + ys <= x, "out_table must not overlap block_table");
+    NEED(tables_apart(block_table, table_stride, out_table, out_stride, rows, table_cols), "out_table must not overlap block_table");
     ReorderArgs a{};
     a.cache = view(S, cache8, cache, page_stride, n_pages, block_table, table_stride, table_cols);
     a.n_layers = n_layers;
