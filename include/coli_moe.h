@@ -581,17 +581,22 @@ coli_status coli_latent_read(coli_serve *serve, int32_t cache_kind, const void *
 
 /* Plan a step whose sequences come in groups that begin with the same tokens: group g
  * is sequences group_start[g] .. group_start[g + 1] - 1 (int32 [n_groups + 1],
- * ascending, within 0..n_seq; sequences before the first group and behind the last are
- * planned as before, and so are those of a group whose prefix_len is 0), of which
- * the first prefix_len[g] positions hold the same rows (on the same pages, or copies of
- * them; the call trusts that, and reads them through one sequence's row of the block
- * table).  The decode calls that follow give what they give after coli_latent_plan, up to
- * the rounding of their sums, and attend to a group's prefix once for all its
- * tokens: to those of its positions that every token of the group sees as context, in
- * whole tiles of 64.  Nothing is shared where the pieces of all sequences and groups
- * would exceed the handle's room (more than four per CU), and in steps of more than 1024
- * sequences and groups or 65536 tokens.  Groups that do not ascend set bit 0 and
- * nothing is shared. */
+ * ascending, within 0..n_seq, n_groups up to n_seq; sequences before the first group and
+ * behind the last are planned as before, and so are those of a group whose prefix_len
+ * is 0), of which the first prefix_len[g] positions hold the same rows (on the same
+ * pages, or copies of them; the call trusts that, and reads them through one sequence's
+ * row of the block table).  The decode calls that follow give what they give after
+ * coli_latent_plan, up to the rounding of their sums, and attend to a group's prefix
+ * once for all its tokens: to those of its positions that every token of the group sees
+ * as context, in whole tiles of 64.  Nothing is shared where the pieces of all
+ * sequences and groups would exceed the handle's room (more than four per CU), and in
+ * steps of more than 1024 sequences and groups or 65536 tokens (whose groups are not
+ * looked at).  Groups that do not ascend set bit 0 and nothing is shared.  Which groups
+ * are worth sharing is for the caller to say: it saves products where the tokens * heads
+ * rows of a sequence leave units of 64 partly empty, and costs partial results.  With
+ * one token a sequence and 16 heads it was the faster from a prefix of 512 tokens on for
+ * 64 sequences and of 4096 for 8 and 256; with 64 heads from 4096 on for 8 sequences,
+ * and hardly ever for more. */
 coli_status coli_latent_plan_shared(coli_serve *serve, const int32_t *q_start, const int32_t *kv_len, int32_t n_seq, int32_t n_tok,
                                     const int32_t *group_start, const int32_t *prefix_len, int32_t n_groups, void *stream);
 
@@ -623,9 +628,10 @@ coli_status coli_beam_select(coli_serve *serve, const void *logits, int64_t logi
  * are copied, in each of n_layers caches (layer_stride apart).  A parent of -1: the
  * place takes a beam that is left over as it is.  (So one call also forks a prompt: its
  * pages are beam 0's, the others' tables hold own pages from that of kv_len on, and all
- * parents are 0.)  Other parents out of range count as -1 and set bit 2; a group
- * of unequal lengths sets bit 0 and stays as it is; where a copy's page is out of range
- * bit 1 is set and nothing copied. */
+ * parents are 0.)  Whole pages of beams that no place continues may then stand in no
+ * row of out_table: they are the caller's to use again.  Other parents out of range
+ * count as -1 and set bit 2; a group of unequal lengths sets bit 0 and stays as it is;
+ * where a copy's page is out of range bit 1 is set and nothing copied. */
 coli_status coli_beam_reorder(coli_serve *serve, int32_t cache_kind, void *cache, int64_t page_stride, int32_t n_pages,
                               int32_t n_layers, int64_t layer_stride, const int32_t *block_table, int64_t table_stride,
                               int32_t table_cols, const int32_t *kv_len, const int32_t *parents, int32_t n_groups, int32_t beams,

@@ -8,19 +8,25 @@
 // in registers.  A second launch, a workgroup to a group, joins the sums of
 // each row and the lists of all rows, the scores taken in 64 bits: the candidates
 // of two beams can lie nearer to each other than the 32-bit roundings of their
-// scores.  (One launch, the join by each group's last workgroup: 32 groups of 8 beams of
+// scores.  The sum in a score's logarithm is of fp32 exponentials, added in fp32 within a
+// chunk, which keeps beams apart to about 1e-7.  (One launch, the join by each group's last workgroup: 32 groups of 8 beams of
 // 151643 logits 77 us, as lists are then handed over past the caches, so 42; one group of
 // 4 beams 9.7 and 10.2 us.)
 //
 // Measured, fp32 logits, keep 16: 32 x 8 x 151643, 155 MB, 36 us and 7 for the join (kernel
-// times; both 42 us called in turn): bound by reading the logits, 4.3 TB/s of 5.0 of a large
-// copy.  1 x 4 x 32000, keep 8: 5 and 4.6 us, two launches and their latencies.
+// times; both 42 us called in turn), 4.3 TB/s where a plain read reaches 7.2: bound by the
+// vector work behind the loads (exponentials, the threshold's and the list's ballots) in 89
+// registers, five workgroups a CU, each with one round of loads.  From bf16 or f16 53 us: half the
+// bytes, in loads half as wide, and the same work after a conversion.  1 x 4 x 32000,
+// keep 8: 5 and 4.6 us, two launches and their latencies.
 //
 // The best of a chunk: a lane's largest value is known from the pass.  The keep-th
 // largest of a wave's 64 lane maxima is a value that keep elements of the wave
-// reach; the largest such value of the four waves is a threshold that few more than
-// keep elements of the chunk reach (keep 16 of 8192 normal logits: 40 to 60), and those
-// are ranked by counting.
+// reach; the largest such value of the four waves is a threshold that a few times
+// keep elements of the chunk reach, and those are ranked by counting.  Of 8192 normal logits
+// 45 to 65 reach it at keep 16, 140 at 32, 290 at 48; at 64, where it is the least of a wave's
+// maxima, 700 to 1000, and one chunk in eight has more than are ranked and takes its maxima
+// one after the other.  32 x 8 x 151643 so takes 61 us at keep 32, 127 at 48 and 860 at 64.
 #include "coli_moe.h"
 #include "dev_attn.h"
 
@@ -191,7 +197,8 @@ __global__ __launch_bounds__(kThreads) void select_kernel(SelectArgs a, int row0
         }
         return;
     }
-    // Many equal logits at the threshold: one maximum after the other.
+    // More at the threshold than are ranked (many equal logits, or keep near 64): one maximum
+    // after the other.
     uint64_t before = ~0ull;
     for (int r = 0; r < keep; ++r) {
         uint64_t k = 0;

@@ -882,6 +882,9 @@ constexpr int kPlanThreads = 1024;
 constexpr int kItemCost = 3;    // tiles: the queries, the first tile's latency and the partial result
 constexpr int kJoinItems = 64;  // pieces whose joining costs as much as a tile
 constexpr int kMinRun = 2;
+// (The costs are those of a 16-bit cache's tiles and of whole 64-row units; steps of an 8-bit
+// cache and units of 32 rows or fewer take others, and pieces that are joined only because
+// their prefix is shared are not counted: the plan does not know of them.)
 constexpr float kTileTime = 1.4f, kPieceTime = 0.06f;   // of 16 pieces' joining
 constexpr int kSortMost = 1024; // sequences that are put in order
 static_assert(kPrefixEntries == kSortMost && kPrefixEntries == kPlanThreads, "an entry to a thread, all of them in LDS");
@@ -898,9 +901,14 @@ __device__ __forceinline__ int cut(int tiles, int per) { return max(1, (tiles + 
 // masked; the sequences begin behind it.  Both leave pieces for the join, which goes by
 // the group's 64-row units and finds each row's own pieces by its token's record: by the
 // sequences' units, of 16 rows each, it read the prefix's pieces four times over (64
-// sequences behind 32000 tokens, 16 heads: 23 us, so 11).  That step: 89 us, 72 GF, of
-// 80 MB where the 64 contexts are 2.4 GB; its plan 29 us, that of eight sequences behind
-// 4096 tokens 15.
+// sequences behind 32000 tokens, 16 heads: 23 us, so 11).  That step: 89 us, 72 GF, 80 MB
+// read; its plan 29 us, that of eight sequences behind 4096 tokens 15.
+// Sharing saves products where the sequences' rows leave units partly empty, and costs an
+// item, two pieces and their join for each unit; the plan does as it is told and does not weigh
+// them.  One token and 500 of their own each, on the same pages, undivided and shared (us, the
+// decode without its plan): 64 sequences of 16 heads behind 512 tokens 27 and 26, 4096 47
+// and 31, 32000 213 and 88; of 64 heads, whose rows fill a unit by themselves, 31 and 30, 58 and
+// 59, 289 and 268; 256 sequences behind 512 tokens 44 and 62 (16 heads), 52 and 83 (64).
 struct Groups {
     const int32_t *start, *prefix;     // [n + 1] first sequences; [n] tokens
     int n;

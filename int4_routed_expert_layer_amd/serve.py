@@ -220,7 +220,7 @@ class Serve:
         With group_start int32 [G + 1] and prefix_len int32 [G] the sequences
         group_start[g] .. group_start[g + 1] - 1 begin with the same prefix_len[g]
         cached tokens, which are attended to once for all of them
-        (coli_latent_plan_shared)."""
+        (coli_latent_plan_shared, which says where that is the faster)."""
         ps, n_seq = self._starts("q_start", q_start)
         pl = self._dense("kv_len", kv_len, torch.int32, (n_seq,))
         if (group_start is None) != (prefix_len is None):
@@ -390,7 +390,8 @@ class Serve:
         continues, -1 for none; kv_len int32 [n_groups * beams], equal within a
         group; block_table [n_groups * beams, cols].  Rows of shared last pages are
         copied within cache ([n_pages, page_size, ...] or [n_layers, ...], all layers
-        in one launch).  Returns the new block table."""
+        in one launch).  Returns the new block table; of whole pages that then stand in
+        none of its rows the caller may dispose."""
         groups, beams = self._sizes("parents", parents, 2)
         pp = self._dense("parents", parents, torch.int32, (groups, beams))
         n = groups * beams
